@@ -78,7 +78,8 @@ typedef enum {
   MAO_ERR_NOT_INITIALIZED = 10 /* a call that needs one-time set-up ran before it */
 } mao_status;
 
-typedef enum { MAO_F32 = 0, MAO_BF16 = 1 } mao_dtype;
+/* MAO_F16: the trained-layer operators only; an optimizer's G is fp32 or bf16. */
+typedef enum { MAO_F32 = 0, MAO_BF16 = 1, MAO_F16 = 2 } mao_dtype;
 
 /* Muon+ normalisation direction applied after orthogonalisation. */
 typedef enum {
@@ -302,6 +303,194 @@ MAO_API mao_status mao_foam_workspace_size(const mao_foam_mat* mats, int32_t cou
 MAO_API mao_status mao_foam_step(const mao_foam_mat* mats, int32_t count, const mao_foam_params* p, void* workspace,
                          size_t ws_bytes, mao_stats* stats, mao_stream_t stream);
 
+/* ------------------------------------------------------------------ trained layers
+ *
+ * The operators that make a weight matrix's gradient: layer norm, the linear layer
+ * y = act(x W^T + b) + residual with W (m x n) stored as the optimizers store it, their
+ * backward passes, and 8-bit checkpoints of activations that the backward passes read.
+ * The linear layer's backward writes (or adds to) the G that mao_*_step takes.
+ *
+ * Conventions, beyond those at the top of this file:
+ *   - A matrix of activations is rows x cols, a row per token, row-major with a leading
+ *     dimension `ld` >= cols (elements).  Its elements are of type `dtype`; cols and ld are
+ *     multiples of 8 and its base is 16-byte aligned, so that every row is.  rows may be
+ *     any number from 0; rows behind the last are not touched.
+ *   - With rows = 0 a forward call does nothing, and a backward call writes zeros to the
+ *     weight's and the bias's gradient (adds nothing, where it accumulates).
+ *   - Products, sums and statistics are held in fp32; results are rounded once to their
+ *     type, to nearest even.  Results do not depend on the order in which blocks run: two
+ *     calls on the same inputs give the same bits.
+ *   - A non-finite input propagates by the formulas.
+ *   - No scratch is kept between calls.  Calls that may overlap on the GPU need workspaces
+ *     of their own.  Every call can be captured into a CUDA graph; a workspace belongs to
+ *     the graph as long as the graph may be replayed.
+ *   - Bounded device waits that gave up are recorded per device in a status word of the
+ *     library, read by mao_layer_status().
+ */
+
+/* Activations; z is the value before the activation. */
+typedef enum {
+  MAO_ACT_NONE = 0,
+  MAO_ACT_RELU = 1,      /* max(z, 0); its derivative at 0 is 0 */
+  MAO_ACT_RELU2 = 2,     /* max(z, 0)^2 */
+  MAO_ACT_GELU = 3,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  MAO_ACT_GELU_TANH = 4, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  MAO_ACT_SILU = 5       /* z / (1 + exp(-z)) */
+} mao_activation;
+
+/*
+ * 8-bit checkpoint of a rows x cols matrix of activations.  A row's columns form blocks of
+ * 32, the last one possibly short.  Element j of a row holds a whole number q in
+ * [-127, 127] at q[row * ld_q + j], its block a byte e at e[row * ld_e + j / 32]; the value
+ * is q 2^(e - 127).  Written from values x with the block's largest magnitude a:
+ *   e = max(floor(log2 a) + 121, 1) (1 where a = 0),
+ *   q = x 2^(127 - e), rounded to nearest even and limited to +-127:
+ * the error is at most 2^(e - 128), half a step, and less than a step where |q| is limited.
+ * A block with a NaN or an infinity gets e = 255, q = 0 and reads back as NaN; e = 0, which
+ * is never written, reads back as zeros.  The power-of-two step makes every value exact in
+ * bf16 (q has 7 bits), and in fp16 where x was fp16.  ld_q is a multiple of 32 and at least
+ * cols, ld_e is at least ceil(cols / 32); q is 16-byte aligned.  The padding of a short
+ * block is written as zeros and never read as data.
+ */
+typedef struct {
+  int8_t* q;
+  uint8_t* e;
+  int64_t ld_q, ld_e;
+} mao_ckpt8;
+
+/* x (rows x cols, fp32 / bf16 / fp16) -> its checkpoint.  HBM-bound, one pass. */
+MAO_API mao_status mao_checkpoint8(const void* x, int32_t dtype, int32_t rows, int32_t cols, int64_t ld_x,
+                                   const mao_ckpt8* c, mao_stream_t stream);
+
+/* y = act(value of c), rounded to y's type: a checkpoint of values before an activation
+ * gives back the activation's output as well. */
+MAO_API mao_status mao_checkpoint8_restore(const mao_ckpt8* c, int32_t rows, int32_t cols, int32_t act, void* y,
+                                           int32_t dtype, int64_t ld_y, mao_stream_t stream);
+
+/*
+ * Layer norm over each row: mean = sum(x) / cols, rstd = (sum((x - mean)^2) / cols + eps)^(-1/2),
+ * y = (x - mean) rstd w + b.  cols <= MAO_LAYER_NORM_MAX_COLS.  w and b have one type
+ * (w_dtype), fp32 or the activations'.  yc, where its q is not NULL, receives the checkpoint
+ * of y as y holds it: the bits that mao_checkpoint8 of y would write.
+ */
+#define MAO_LAYER_NORM_MAX_COLS 32768
+
+typedef struct {
+  int32_t rows, cols;
+  int32_t dtype;       /* of x and y: fp32, bf16 or fp16 */
+  int32_t w_dtype;     /* of w and b: MAO_F32 or dtype */
+  const void* x;
+  int64_t ld_x;
+  const void* w;       /* cols */
+  const void* b;       /* cols, or NULL */
+  float eps;           /* >= 0 */
+  void* y;
+  int64_t ld_y;
+  float* mean;         /* rows */
+  float* rstd;         /* rows */
+  mao_ckpt8 yc;        /* q = NULL: none */
+} mao_layer_norm_args;
+
+MAO_API mao_status mao_layer_norm(const mao_layer_norm_args* a, mao_stream_t stream);
+
+/*
+ * Layer norm's gradient, with h = (x - mean) rstd and u = dy w:
+ *   dx = rstd (u - mean(u) - h mean(u h)) + dres,   dw = sum over rows of dy h,   db = sum of dy.
+ * x is the forward input, or its checkpoint (x = NULL, xc.q not NULL).  dres, where not NULL,
+ * is the gradient that reaches x past the norm (the residual stream's).  dw and db are fp32
+ * and overwritten; either may be NULL.
+ */
+typedef struct {
+  int32_t rows, cols;
+  int32_t dtype;       /* of dy, x, dres and dx */
+  int32_t w_dtype;     /* of w */
+  const void* dy;
+  int64_t ld_dy;
+  const void* x;       /* NULL: read xc */
+  int64_t ld_x;
+  mao_ckpt8 xc;
+  const void* w;
+  const float* mean;
+  const float* rstd;
+  const void* dres;    /* or NULL */
+  int64_t ld_dres;
+  void* dx;
+  int64_t ld_dx;
+  float* dw;           /* cols, or NULL */
+  float* db;           /* cols, or NULL */
+} mao_layer_norm_backward_args;
+
+MAO_API mao_status mao_layer_norm_backward_workspace_size(const mao_layer_norm_backward_args* a, size_t* bytes);
+MAO_API mao_status mao_layer_norm_backward(const mao_layer_norm_backward_args* a, void* workspace, size_t ws_bytes,
+                                           mao_stream_t stream);
+
+/*
+ * Linear layer: z = x W^T + b, y = act(z) + residual, with x (rows x n), W (m x n, rows
+ * contiguous with leading dimension n) and y (rows x m), bf16 or fp16 operands on the tensor
+ * cores with fp32 accumulation.  zc, where its q is not NULL, receives the checkpoint of z,
+ * taken from the fp32 sums.  z, where not NULL, receives z in the activations' type.
+ */
+typedef struct {
+  int32_t rows, n, m;
+  int32_t dtype;       /* of x, W, residual, y, z: bf16 or fp16 */
+  const void* x;
+  int64_t ld_x;
+  const void* W;
+  const void* b;       /* m, or NULL */
+  int32_t b_dtype;     /* MAO_F32 or dtype */
+  int32_t act;         /* mao_activation */
+  const void* res;     /* rows x m, or NULL */
+  int64_t ld_res;
+  void* y;
+  int64_t ld_y;
+  void* z;             /* rows x m, or NULL */
+  int64_t ld_z;
+  mao_ckpt8 zc;        /* q = NULL: none */
+} mao_linear_args;
+
+MAO_API mao_status mao_linear_workspace_size(const mao_linear_args* a, size_t* bytes);
+MAO_API mao_status mao_linear(const mao_linear_args* a, void* workspace, size_t ws_bytes, mao_stream_t stream);
+
+/*
+ * The linear layer's gradient (the residual's own gradient is dy):
+ *   dz = dy act'(z),   dx = dz W,   dW (+)= dz^T x,   db = sum over rows of dz.
+ * dz is rounded to the activations' type before the two products (their tensor-core
+ * operands have that type); db sums the unrounded values.  x and z are read from tensors or,
+ * where those are NULL, from their checkpoints; z is not read for MAO_ACT_NONE.  dW is fp32
+ * or of the activations' type, m x n with rows contiguous; `accumulate` adds to an fp32 dW
+ * what this call computes.  dx, dW and db may each be NULL.
+ */
+typedef struct {
+  int32_t rows, n, m;
+  int32_t dtype;       /* of dy, x, W, z, dx: bf16 or fp16 */
+  const void* dy;
+  int64_t ld_dy;
+  const void* x;       /* NULL: read xc */
+  int64_t ld_x;
+  mao_ckpt8 xc;
+  const void* W;
+  int32_t act;
+  const void* z;       /* NULL: read zc */
+  int64_t ld_z;
+  mao_ckpt8 zc;
+  void* dx;
+  int64_t ld_dx;
+  void* dW;
+  int32_t dw_dtype;    /* MAO_F32 or dtype */
+  int32_t accumulate;  /* 1: dW += (fp32 only) */
+  float* db;           /* m */
+} mao_linear_backward_args;
+
+MAO_API mao_status mao_linear_backward_workspace_size(const mao_linear_backward_args* a, size_t* bytes);
+MAO_API mao_status mao_linear_backward(const mao_linear_backward_args* a, void* workspace, size_t ws_bytes,
+                                       mao_stream_t stream);
+
+/* Synchronises `stream` and returns MAO_OK, or the first condition that the trained-layer
+ * operators recorded on the current device since the last call of this function
+ * (MAO_ERR_TIMEOUT: a bounded wait gave up, and the call's outputs are not complete);
+ * `where` (nullable) receives its site.  Reading clears it. */
+MAO_API mao_status mao_layer_status(mao_stream_t stream, int32_t* where);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Optimizer-state element counts per matrix ("Factored One-sided Adam-Moment"
@@ -349,7 +538,17 @@ typedef enum {
   MAO_K_PC_QR_APPLY = 23,    /* QR panel products W R^{-1} (tensor cores) */
   MAO_K_PC_QR_REDUCE = 24,   /* sum of the K-slice partials of the projection coefficients */
   MAO_K_PC_STATS = 25,       /* per-matrix diagnostics of a SOAP / FOAM step */
-  MAO_K_MOP_INIT = 26        /* exact polar factor: fp32 X0 = M / (||M||_F + eps) and its planes (HBM) */
+  MAO_K_MOP_INIT = 26,       /* exact polar factor: fp32 X0 = M / (||M||_F + eps) and its planes (HBM) */
+  MAO_K_CKPT8 = 27,          /* 8-bit checkpoint written (HBM) */
+  MAO_K_CKPT8_RESTORE = 28,  /* 8-bit checkpoint read back (HBM) */
+  MAO_K_LAYER_NORM = 29,     /* layer norm (HBM) */
+  MAO_K_LAYER_NORM_BWD = 30, /* its gradient, partial column sums included (HBM) */
+  MAO_K_COL_REDUCE = 31,     /* sum of partial column sums */
+  MAO_K_LINEAR = 32,         /* x W^T with its epilogue (tensor cores) */
+  MAO_K_LINEAR_DX = 33,      /* dz W (tensor cores) */
+  MAO_K_LINEAR_DW = 34,      /* dz^T x (tensor cores) */
+  MAO_K_ACT_BWD = 35,        /* dz = dy act'(z) with partial column sums (HBM) */
+  MAO_K_SLICE_REDUCE = 36    /* sum of a product's K slices, with its epilogue */
 } mao_kernel_id;
 
 /* What one recorded launch was: its kernel and its algorithmic work (useful

@@ -25,7 +25,9 @@ MAO_ERR_TIMEOUT = 8
 MAO_ERR_UNSUPPORTED = 9
 MAO_ERR_NOT_INITIALIZED = 10
 
-MAO_F32, MAO_BF16 = 0, 1
+MAO_F32, MAO_BF16, MAO_F16 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
+LAYER_NORM_MAX_COLS = 32768
 NORM_MODES = {"none": 0, "row": 1, "col": 2, "col_row": 3, "row_col": 4}
 REFRESH_EVERY_K, REFRESH_ADAPTIVE, REFRESH_NEVER = 0, 1, 2
 POLAR_NS, POLAR_EXACT = 0, 1
@@ -73,6 +75,38 @@ class FoamParams(ctypes.Structure):
                 ("t", c_int64), ("refresh", Refresh), ("tau_raw_trace", c_int32)]
 
 
+class Ckpt8(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("e", c_void_p), ("ld_q", c_int64), ("ld_e", c_int64)]
+
+
+class LayerNormArgs(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("cols", c_int32), ("dtype", c_int32), ("w_dtype", c_int32), ("x", c_void_p),
+                ("ld_x", c_int64), ("w", c_void_p), ("b", c_void_p), ("eps", c_float), ("y", c_void_p),
+                ("ld_y", c_int64), ("mean", c_void_p), ("rstd", c_void_p), ("yc", Ckpt8)]
+
+
+class LayerNormBackwardArgs(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("cols", c_int32), ("dtype", c_int32), ("w_dtype", c_int32), ("dy", c_void_p),
+                ("ld_dy", c_int64), ("x", c_void_p), ("ld_x", c_int64), ("xc", Ckpt8), ("w", c_void_p),
+                ("mean", c_void_p), ("rstd", c_void_p), ("dres", c_void_p), ("ld_dres", c_int64), ("dx", c_void_p),
+                ("ld_dx", c_int64), ("dw", c_void_p), ("db", c_void_p)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("n", c_int32), ("m", c_int32), ("dtype", c_int32), ("x", c_void_p),
+                ("ld_x", c_int64), ("W", c_void_p), ("b", c_void_p), ("b_dtype", c_int32), ("act", c_int32),
+                ("res", c_void_p), ("ld_res", c_int64), ("y", c_void_p), ("ld_y", c_int64), ("z", c_void_p),
+                ("ld_z", c_int64), ("zc", Ckpt8)]
+
+
+class LinearBackwardArgs(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("n", c_int32), ("m", c_int32), ("dtype", c_int32), ("dy", c_void_p),
+                ("ld_dy", c_int64), ("x", c_void_p), ("ld_x", c_int64), ("xc", Ckpt8), ("W", c_void_p),
+                ("act", c_int32), ("z", c_void_p), ("ld_z", c_int64), ("zc", Ckpt8), ("dx", c_void_p),
+                ("ld_dx", c_int64), ("dW", c_void_p), ("dw_dtype", c_int32), ("accumulate", c_int32),
+                ("db", c_void_p)]
+
+
 class LaunchInfo(ctypes.Structure):
     _fields_ = [("kernel", c_int32), ("pad", c_int32), ("flops", ctypes.c_double), ("bytes", ctypes.c_double),
                 ("tc_flops", ctypes.c_double), ("exec_flops", ctypes.c_double), ("exec_tc_flops", ctypes.c_double)]
@@ -82,7 +116,9 @@ KERNEL_NAMES = {1: "muon_prep", 2: "muon_scale", 3: "ns_gram", 4: "ns_poly", 5: 
                 7: "muon_colscale", 8: "muon_rowscale", 9: "muon_update", 10: "muon_stats", 11: "split3",
                 12: "gemm_test", 13: "pc_elementwise", 14: "pc_factor", 15: "pc_check", 16: "pc_power",
                 17: "pc_sort", 18: "pc_qr", 19: "pc_rotate", 20: "pc_update", 21: "pc_panel", 22: "pc_chol",
-                23: "pc_qr_apply", 24: "pc_qr_reduce", 25: "pc_stats", 26: "mop_init"}
+                23: "pc_qr_apply", 24: "pc_qr_reduce", 25: "pc_stats", 26: "mop_init", 27: "ckpt8",
+                28: "ckpt8_restore", 29: "layer_norm", 30: "layer_norm_bwd", 31: "col_reduce", 32: "linear",
+                33: "linear_dx", 34: "linear_dw", 35: "act_bwd", 36: "slice_reduce"}
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -97,6 +133,17 @@ SIGNATURES = {
     "mao_foam_workspace_size": (c_int32, [POINTER(FoamMat), c_int32, POINTER(FoamParams), POINTER(c_size_t)]),
     "mao_foam_step": (c_int32, [POINTER(FoamMat), c_int32, POINTER(FoamParams), c_void_p, c_size_t, c_void_p,
                                 c_void_p]),
+    "mao_checkpoint8": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int64, POINTER(Ckpt8), c_void_p]),
+    "mao_checkpoint8_restore": (c_int32, [POINTER(Ckpt8), c_int32, c_int32, c_int32, c_void_p, c_int32, c_int64,
+                                          c_void_p]),
+    "mao_layer_norm": (c_int32, [POINTER(LayerNormArgs), c_void_p]),
+    "mao_layer_norm_backward_workspace_size": (c_int32, [POINTER(LayerNormBackwardArgs), POINTER(c_size_t)]),
+    "mao_layer_norm_backward": (c_int32, [POINTER(LayerNormBackwardArgs), c_void_p, c_size_t, c_void_p]),
+    "mao_linear_workspace_size": (c_int32, [POINTER(LinearArgs), POINTER(c_size_t)]),
+    "mao_linear": (c_int32, [POINTER(LinearArgs), c_void_p, c_size_t, c_void_p]),
+    "mao_linear_backward_workspace_size": (c_int32, [POINTER(LinearBackwardArgs), POINTER(c_size_t)]),
+    "mao_linear_backward": (c_int32, [POINTER(LinearBackwardArgs), c_void_p, c_size_t, c_void_p]),
+    "mao_layer_status": (c_int32, [c_void_p, POINTER(c_int32)]),
     "mao_muon_state_elems": (c_uint64, [c_int32, c_int32]),
     "mao_soap_state_elems": (c_uint64, [c_int32, c_int32]),
     "mao_foam_state_elems": (c_uint64, [c_int32, c_int32]),

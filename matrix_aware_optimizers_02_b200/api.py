@@ -5,6 +5,9 @@ every arithmetic step runs in the library's kernels.
     from matrix_aware_optimizers_02_b200 import api
     step = api.MuonBatch([(W, G, M), ...], mu=0.95, lr=0.02, norm="col_row")
     step()            # one optimizer step on torch.cuda.current_stream()
+
+The trained layers that make the gradients G (layer_norm, linear, their backward passes
+and 8-bit activation checkpoints) are in layers.py and offered here as well.
 """
 
 from __future__ import annotations
@@ -15,6 +18,8 @@ from typing import Iterable, Optional, Sequence, Tuple
 import torch
 
 from . import _lib as L
+from .layers import (Checkpoint8, checkpoint8, layer_norm, layer_norm_backward, layer_status, linear,  # noqa: F401
+                     linear_backward)
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:

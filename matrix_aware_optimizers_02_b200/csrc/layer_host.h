@@ -1,0 +1,42 @@
+// Host side shared by the trained-layer entry points: argument checks and the
+// operators that one entry point calls of another.
+#pragma once
+
+#include <climits>
+
+#include "host_common.h"
+#include "layer_math.cuh"
+
+namespace mao {
+
+inline int elem_size(int dtype) { return dtype == MAO_F32 ? 4 : 2; }
+inline int ckpt_blocks(int cols) { return (cols + 31) / 32; }
+inline bool is16(int dtype) { return dtype == MAO_BF16 || dtype == MAO_F16; }
+
+// rows x cols of activations with the module's row rule (see "trained layers" in mao.h)
+inline mao_status check_acts(const void* p, int rows, int cols, long long ld) {
+  if (rows > 0 && p == nullptr) return MAO_ERR_INVALID_ARG;
+  if (ld < cols || (ld & 7) || ld > (1ll << 36)) return MAO_ERR_SHAPE;
+  return aligned16(p) ? MAO_OK : MAO_ERR_ALIGN;
+}
+inline mao_status check_dims(int rows, int cols) {
+  return (rows < 0 || cols < 1 || (cols & 7)) ? MAO_ERR_SHAPE : MAO_OK;
+}
+inline mao_status check_ckpt(const mao_ckpt8& c, int rows, int cols) {
+  if (rows > 0 && (c.q == nullptr || c.e == nullptr)) return MAO_ERR_INVALID_ARG;
+  if (c.ld_q < cols || (c.ld_q & 31) || c.ld_q > (1ll << 36) || c.ld_e < ckpt_blocks(cols) || c.ld_e > (1ll << 36))
+    return MAO_ERR_SHAPE;
+  return aligned16(c.q) ? MAO_OK : MAO_ERR_ALIGN;
+}
+inline CkptView view(const mao_ckpt8& c) { return CkptView{c.q, c.e, c.ld_q, c.ld_e}; }
+
+inline mao_status launched() { return cudaGetLastError() == cudaSuccess ? MAO_OK : MAO_ERR_CUDA; }
+
+// y = act(value of c); arguments checked by the caller, rows >= 1
+mao_status restore_launch(const CkptView& c, int rows, int cols, int act, void* y, int dtype, long long ld_y,
+                          cudaStream_t stream);
+
+// out[col] = sum over parts of part[p * cols + col], in a fixed order
+mao_status col_reduce_launch(const float* part, int parts, int cols, float* out, cudaStream_t stream);
+
+}  // namespace mao

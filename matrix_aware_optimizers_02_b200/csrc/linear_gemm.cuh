@@ -1,0 +1,521 @@
+// The trained layers' matrix products for sm_100a: D = A B^T with 16-bit operands (bf16 or
+// fp16), fp32 accumulation in tensor memory, and the linear layer's epilogues.
+//
+//   forward    y  = act(x W^T + b) + res   A = x (K-major),      B = W (K-major)
+//   dx         dx = dz W                   A = dz (K-major),     B = W (MN-major)
+//   dW         dW = dz^T x                 A = dz (MN-major),    B = x (MN-major)
+//
+// One persistent kernel, one CTA per SM or one CTA pair per two SMs, walking work items
+// (output tile, K slice) with a static stride.  Warp roles (320 threads):
+//   warp 0     TMA producer (one lane): a ring of 128-byte-swizzled A / B tiles;
+//   warp 1     owner of the tensor memory and MMA issuer (one lane);
+//   warps 2-9  epilogue, two per tensor-memory lane quarter, half of the columns each.
+// Two accumulators let an item's epilogue overlap the next item's MMAs.
+//
+// Tiles.  PAIR: 256 x 256 per CTA pair (tcgen05.mma.cta_group::2); each CTA loads 128 rows
+// of A and 128 of B's 256, 64 operand bytes per clock of tensor work against 96 for a
+// one-CTA 128 x 256 tile, which leaves shared memory room to refill.  One CTA: 128 x 128,
+// for products whose 256 x 256 tiles would leave most SMs idle.  K is cut into slices when
+// even those are too few: each slice leaves fp32 partial sums in the workspace and a second
+// kernel joins them in slice order and runs the same epilogue.
+//
+// Order.  Tiles run in bands of kBandRows tile rows, column by column inside a band, so the
+// tiles that are in flight together share few operand rows and columns in L2.
+//
+// Accuracy.  The tensor core's accumulation truncates: its error grows with every add.  16-bit
+// results accumulate the whole K (the error stays far below their rounding); an fp32 dW
+// accumulates kFoldBlocks * 64 of K in tensor memory at a time, and the epilogue adds
+// those sums in fp32 registers, rounded to nearest.
+#pragma once
+
+#include "gemm_tc.cuh"
+#include "layer_math.cuh"
+
+namespace mao {
+
+// Where a bounded wait of these kernels records that it gave up; sticky until read.
+static __device__ DevStatus g_layer_status;
+
+constexpr int kBandRows = 8;
+constexpr int kFoldBlocks = 16;
+
+enum LinKind : int {
+  LIN_FORWARD = 0,  // bias, activation, residual, checkpoint of z
+  LIN_STORE = 1,    // out (16-bit) = acc
+  LIN_GRAD32 = 2,   // out (fp32) = acc, or += acc
+};
+
+struct LinEpilogue {
+  void* out;
+  const void* bias;
+  const void* res;
+  void* z;
+  CkptView k;
+  long long ld_out, ld_res, ld_z;
+  int M, N;
+  int act;
+  int bias_f32;
+  int accumulate;
+};
+
+struct LinParams {
+  CUtensorMap mapA, mapB;
+  LinEpilogue e;
+  float* part;  // [slice][M][N] partial sums when slices > 1
+  int tiles_m, tiles_n;
+  int items;  // tiles * slices
+  int slices;
+  int nk;     // k-blocks of 64
+  int slice_blocks;
+};
+
+// ------------------------------------------------------------------ epilogue
+template <int ACT>
+__device__ __forceinline__ void act32(float* v) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = act_value<ACT>(v[j]);
+}
+
+// 32 consecutive 16-bit elements of one row, `n` of them valid (a multiple of 8)
+template <class T>
+__device__ __forceinline__ void store16x32(T* dst, const float* v, int n) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = Elem<T>::pack(v[2 * j], v[2 * j + 1]);
+  if (n >= 32 && aligned32(dst)) {
+    st_global_v8(dst, w);
+    st_global_v8(dst + 16, w + 8);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (8 * j < n) reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+}
+
+// The epilogue of 32 consecutive columns [col, col + 32) of one row; v holds the sums.
+// Columns come in eights (N is a multiple of 8).
+template <class T, int KIND>
+__device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int col, float* v) {
+  if (row >= e.M || col >= e.N) return;
+  const int n = min(32, e.N - col);
+  if constexpr (KIND == LIN_GRAD32) {
+    float* o = static_cast<float*>(e.out) + (long long)row * e.ld_out + col;
+    if (e.accumulate) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        if (j < n) {
+          const float4 a = *reinterpret_cast<const float4*>(o + j);
+          v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w;
+        }
+    }
+    if (n == 32) {
+      store_f32x32(o, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        if (j < n) *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+  } else if constexpr (KIND == LIN_STORE) {
+    store16x32<T>(static_cast<T*>(e.out) + (long long)row * e.ld_out + col, v, n);
+  } else {
+    if (e.bias != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 8)
+        if (j < n) {
+          float b[8];
+          load_param8<T>(e.bias, e.bias_f32, col + j, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[j + i] += b[i];
+        }
+    }
+    if (e.z != nullptr) store16x32<T>(static_cast<T*>(e.z) + (long long)row * e.ld_z + col, v, n);
+    if (e.k.q != nullptr) {
+      // this thread's 32 columns are one block of the checkpoint; columns behind the last
+      // hold zeros (the operands' out-of-range rows load as zeros, and the bias skips them)
+      uint32_t a = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) a = max(a, abs_bits(v[j]));
+      const uint32_t ex = ckpt_exponent(a);
+      const float inv = ckpt_inverse(ex);
+      const uint32_t mask = ex == 255u ? 0u : 0xffffffffu;
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = ckpt_q4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv, mask);
+      int8_t* q = e.k.q + (long long)row * e.k.ld_q + col;
+      if (aligned32(q)) {
+        st_global_v8(q, w);
+      } else {
+        reinterpret_cast<uint4*>(q)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(q)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      e.k.e[(long long)row * e.k.ld_e + (col >> 5)] = (uint8_t)ex;
+    }
+    switch (e.act) {
+      case MAO_ACT_RELU: act32<MAO_ACT_RELU>(v); break;
+      case MAO_ACT_RELU2: act32<MAO_ACT_RELU2>(v); break;
+      case MAO_ACT_GELU: act32<MAO_ACT_GELU>(v); break;
+      case MAO_ACT_GELU_TANH: act32<MAO_ACT_GELU_TANH>(v); break;
+      case MAO_ACT_SILU: act32<MAO_ACT_SILU>(v); break;
+      default: break;
+    }
+    if (e.res != nullptr) {
+      const T* r = static_cast<const T*>(e.res) + (long long)row * e.ld_res + col;
+#pragma unroll
+      for (int j = 0; j < 32; j += 8)
+        if (j < n) {
+          Vec8<T> x;
+          x.load(r + j);
+          float f[8];
+          x.get(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[j + i] += f[i];
+        }
+    }
+    store16x32<T>(static_cast<T*>(e.out) + (long long)row * e.ld_out + col, v, n);
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <bool PAIR>
+struct LinCfg {
+  static constexpr int BM = PAIR ? 256 : 128;  // tile rows (128 per CTA)
+  static constexpr int BN = PAIR ? 256 : 128;  // tile columns
+  static constexpr int BK = 64;
+  static constexpr int A_TILE = 128 * 128;  // bytes: 128 rows of 64 elements per CTA
+  static constexpr int B_TILE = 128 * 128;  // PAIR: half of B's rows per CTA
+  static constexpr int STAGE_BYTES = A_TILE + B_TILE;
+  static constexpr int STAGES = 6;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int COLS = BN / 2;  // columns per epilogue warp
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+};
+
+struct LinItem {
+  int m0, n0;    // first row / column of the tile
+  int kb0, kb1;  // its k-blocks
+  int slice;
+};
+
+template <bool PAIR>
+__device__ __forceinline__ LinItem lin_item(const LinParams& p, int item) {
+  using Cfg = LinCfg<PAIR>;
+  const int tiles = p.tiles_m * p.tiles_n;
+  LinItem t;
+  t.slice = item / tiles;
+  const int tile = item - t.slice * tiles;
+  const int band = tile / (kBandRows * p.tiles_n);
+  const int first = band * kBandRows;
+  const int rows = min(kBandRows, p.tiles_m - first);
+  const int r = tile - band * kBandRows * p.tiles_n;
+  const int c = r / rows;
+  t.n0 = c * Cfg::BN;
+  t.m0 = (first + r - c * rows) * Cfg::BM;
+  t.kb0 = t.slice * p.slice_blocks;
+  t.kb1 = min(p.nk, t.kb0 + p.slice_blocks);
+  return t;
+}
+
+// One operand's share of a stage: 128 rows (K-major) or 128 columns of 64 K rows (MN-major).
+template <bool PAIR, int MN_MAJOR>
+__device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t bar_lead,
+                                         int k0, int mn0) {
+  if constexpr (!MN_MAJOR) {
+    if constexpr (PAIR) tma_load_3d_pair(dst, map, bar_lead, k0, mn0, 0);
+    else tma_load_3d(dst, map, bar, k0, mn0, 0);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if constexpr (PAIR) tma_load_3d_pair(dst + c * 64 * 128, map, bar_lead, mn0 + c * 64, k0, 0);
+      else tma_load_3d(dst + c * 64 * 128, map, bar, mn0 + c * 64, k0, 0);
+    }
+  }
+}
+
+template <class T, int KIND, int A_MN, int B_MN, bool PAIR>
+__device__ __forceinline__ void lin_body(const LinParams& p) {
+  using Cfg = LinCfg<PAIR>;
+  constexpr int STAGES = Cfg::STAGES, BK = Cfg::BK;
+  constexpr uint32_t IDESC = make_idesc(Elem<T>::kDtype == MAO_BF16 ? 1u : 0u, A_MN, B_MN, Cfg::BM, Cfg::BN);
+  constexpr int FOLD = KIND == LIN_GRAD32 ? kFoldBlocks : (1 << 30);  // k-blocks per accumulation
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[STAGES];
+  __shared__ __align__(8) uint64_t tfull_bar[2];
+  __shared__ __align__(8) uint64_t tempty_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  __shared__ int prod_it_sh, mma_it_sh;
+
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int workers = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  DevStatus* status = &g_layer_status;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull_bar[a], 1);
+      mbar_init(&tempty_bar[a], (PAIR ? 2 : 1) * 32 * Cfg::EPI_WARPS);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_sh = 0;
+    prod_it_sh = 0;
+    mma_it_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&tmem_base_sh, Cfg::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&tmem_base_sh, Cfg::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.mapA);
+    tma_prefetch_desc(&p.mapB);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+  volatile int* abort_flag = &abort_sh;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- producer
+      int it = 0;
+      bool ok = true;
+      for (int item = worker; item < p.items && ok; item += workers) {
+        const LinItem t = lin_item<PAIR>(p, item);
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1;
+          if (!mbar_wait(&empty_bar[s], ph ^ 1, status, 51, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * Cfg::STAGE_BYTES;
+          uint32_t lead = 0;
+          if constexpr (PAIR) {
+            if (leader) mbar_arrive_expect_tx(&full_bar[s], 2 * Cfg::STAGE_BYTES);
+            lead = mapa_shared(smem_u32(&full_bar[s]), 0);
+          } else {
+            mbar_arrive_expect_tx(&full_bar[s], Cfg::STAGE_BYTES);
+          }
+          lin_load<PAIR, A_MN>(st, &p.mapA, &full_bar[s], lead, kb * BK, t.m0 + 128 * (int)rank);
+          lin_load<PAIR, B_MN>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK, t.n0 + 128 * (int)rank);
+        }
+      }
+      prod_it_sh = it;
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // -------------------------------------------------------------- MMA issuer
+      int it = 0, used = 0;
+      bool ok = true;
+      for (int item = worker; item < p.items && ok; item += workers) {
+        const LinItem t = lin_item<PAIR>(p, item);
+        for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += FOLD) {
+          const int c1 = (t.kb1 - c0 > FOLD) ? c0 + FOLD : t.kb1;
+          const int acc = used & 1;
+          const uint32_t aph = (used >> 1) & 1;
+          ++used;
+          if (!mbar_wait(&tempty_bar[acc], aph ^ 1, status, 52, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * Cfg::BN;
+          for (int kb = c0; kb < c1; ++kb, ++it) {
+            const int s = it % STAGES;
+            if (!mbar_wait(&full_bar[s], (it / STAGES) & 1, status, 53, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(smem + s * Cfg::STAGE_BYTES);
+            const uint32_t b_base = a_base + Cfg::A_TILE;
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint64_t ad = operand_desc<A_MN, 128, 2>(a_base, k), bd = operand_desc<B_MN, 128, 2>(b_base, k);
+              const uint32_t accum = (kb > c0 || k > 0) ? 1u : 0u;
+              if constexpr (PAIR) umma_f16_pair(d_tmem, ad, bd, IDESC, accum);
+              else umma_f16(d_tmem, ad, bd, IDESC, accum);
+            }
+            if constexpr (PAIR) umma_commit_pair(&empty_bar[s], 0x3);
+            else umma_commit(&empty_bar[s]);
+          }
+          if (!ok) break;
+          if constexpr (PAIR) umma_commit_pair(&tfull_bar[acc], 0x3);
+          else umma_commit(&tfull_bar[acc]);
+        }
+      }
+      mma_it_sh = it;
+      // every MMA issued here has finished before tensor memory is released
+      if constexpr (PAIR) umma_commit_pair(&drain_bar, 0x3);
+      else umma_commit(&drain_bar);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    constexpr int COLS = Cfg::COLS;
+    const int q = warp & 3;                   // tensor-memory lane quarter this warp may read
+    const int cb = ((warp - 2) >> 2) * COLS;  // its first column
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cb;
+    uint32_t tempty_lead[2] = {0, 0};
+    if constexpr (PAIR) {
+      tempty_lead[0] = mapa_shared(smem_u32(&tempty_bar[0]), 0);
+      tempty_lead[1] = mapa_shared(smem_u32(&tempty_bar[1]), 0);
+    }
+    int used = 0;
+    bool ok = true;
+    for (int item = worker; item < p.items && ok; item += workers) {
+      const LinItem t = lin_item<PAIR>(p, item);
+      const int row = t.m0 + 128 * (int)rank + q * 32 + lane;
+      const int col = t.n0 + cb;
+      // what a 32-column chunk becomes: partial sums of a K slice, or the result
+      auto finish = [&](int c, float* v) {
+        if (p.slices > 1) {
+          const int n = min(32, p.e.N - c);
+          if (row < p.e.M && n > 0) {
+            float* o = p.part + ((long long)t.slice * p.e.M + row) * p.e.N + c;
+            if (n == 32) {
+              store_f32x32(o, v);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                if (j < n) *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            }
+          }
+        } else {
+          lin_epilogue<T, KIND>(p.e, row, c, v);
+        }
+      };
+      if constexpr (KIND != LIN_GRAD32) {
+        const int acc = used & 1;
+        const bool w = mbar_wait(&tfull_bar[acc], (used >> 1) & 1, status, 54, abort_flag);
+        ++used;
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < COLS / 32; ++ch) {
+          uint32_t rr[32];
+          tmem_ld_32x32b_x32(lane_base + acc * Cfg::BN + ch * 32, rr);
+          tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(rr[j]);
+          finish(col + ch * 32, v);
+        }
+        tc_fence_before();
+        if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty_lead[acc]);
+        else mbar_arrive_relaxed(&tempty_bar[acc]);
+      } else {
+        float run[COLS];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) run[j] = 0.0f;
+        for (int c0 = t.kb0; c0 < t.kb1; c0 += FOLD) {
+          const int acc = used & 1;
+          const bool w = mbar_wait(&tfull_bar[acc], (used >> 1) & 1, status, 54, abort_flag);
+          ++used;
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int ch = 0; ch < COLS / 32; ++ch) {
+            uint32_t rr[32];
+            tmem_ld_32x32b_x32(lane_base + acc * Cfg::BN + ch * 32, rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) run[ch * 32 + j] += __uint_as_float(rr[j]);
+          }
+          tc_fence_before();
+          if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty_lead[acc]);
+          else mbar_arrive_relaxed(&tempty_bar[acc]);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int ch = 0; ch < COLS / 32; ++ch) finish(col + ch * 32, &run[ch * 32]);
+      }
+    }
+  }
+
+  // ------------------------------------------------------------------ teardown
+  if (warp == 1 && lane == 0) mbar_wait(&drain_bar, 0, status, 55, abort_flag, false);
+  __syncthreads();
+  if (leader && warp == 0 && lane == 0) {
+    // after an early exit, let the loads in flight land before the CTA ends: the first
+    // CTA's full barriers count both CTAs' bytes, and no producer runs more than STAGES
+    // loads ahead of the MMAs
+    const int last = max(prod_it_sh, mma_it_sh + (PAIR && *abort_flag ? STAGES : 0));
+    for (int j = mma_it_sh; j < last; ++j)
+      mbar_wait(&full_bar[j % STAGES], (j / STAGES) & 1, status, 56, abort_flag, false);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+    else tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+  }
+}
+
+template <class T, int KIND, int A_MN, int B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
+    lin_pair_kernel(const __grid_constant__ LinParams p) {
+  lin_body<T, KIND, A_MN, B_MN, true>(p);
+}
+
+template <class T, int KIND, int A_MN, int B_MN>
+__global__ void __launch_bounds__(320, 1) lin_kernel(const __grid_constant__ LinParams p) {
+  lin_body<T, KIND, A_MN, B_MN, false>(p);
+}
+
+// Joins the K slices in slice order and runs the epilogue.  A thread owns 32 columns of a
+// row, as in the product kernel.
+template <class T, int KIND>
+__global__ void __launch_bounds__(128) lin_reduce_kernel(const LinEpilogue e, const float* __restrict__ part,
+                                                         int slices, int col_blocks, long long total) {
+  const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+  if (i >= total) return;
+  const int row = (int)(i / col_blocks);
+  const int col = (int)(i - (long long)row * col_blocks) * 32;
+  const int n = min(32, e.N - col);
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+  const float* s = part + (long long)row * e.N + col;
+  for (int k = 0; k < slices; ++k, s += (long long)e.M * e.N) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+      if (j < n) {
+        const float4 a = *reinterpret_cast<const float4*>(s + j);
+        v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w;
+      }
+  }
+  lin_epilogue<T, KIND>(e, row, col, v);
+}
+
+}  // namespace mao
