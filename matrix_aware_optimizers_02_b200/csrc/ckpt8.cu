@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(CkptView k, T* __rest
     float f[8];
     v[u].get(f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = act_value<ACT>(f[j]);
+    for (int j = 0; j < 8; ++j) f[j] = act_value<ACT, sizeof(T) == 4>(f[j]);
     Vec8<T> o;
     o.set(f);
     o.store(y + s.row * ld_y + s.col);

@@ -36,7 +36,8 @@ inline mao_status launched() { return cudaGetLastError() == cudaSuccess ? MAO_OK
 mao_status restore_launch(const CkptView& c, int rows, int cols, int act, void* y, int dtype, long long ld_y,
                           cudaStream_t stream);
 
-// out[col] = sum over parts of part[p * cols + col], in a fixed order
-mao_status col_reduce_launch(const float* part, int parts, int cols, float* out, cudaStream_t stream);
+// out0[col] = sum over parts of part[p * cols + col], in a fixed order; out1 likewise of the
+// parts * cols values behind.  Either may be nullptr.
+mao_status col_reduce_launch(const float* part, int parts, int cols, float* out0, float* out1, cudaStream_t stream);
 
 }  // namespace mao

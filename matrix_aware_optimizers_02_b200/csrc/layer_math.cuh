@@ -100,6 +100,55 @@ __device__ __forceinline__ void load_param8(const void* p, bool f32, long long i
   }
 }
 
+// ------------------------------------------------------------------ asynchronous loads
+// A thread's own ring in shared memory: cp.async of 16 (or 8) bytes that only the issuing
+// thread reads back, so no barrier orders them, only its own wait.  With ok false nothing is
+// read and zeros are written.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the latest N groups of this thread have landed
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// One vector of 8 elements per thread in a ring slot: 16-byte pieces `stride` bytes apart
+// (a block's threads side by side, so neighbouring lanes touch neighbouring banks).
+template <class T>
+struct Slot8 {
+  static constexpr int kBytes = 8 * sizeof(T);
+  static __device__ __forceinline__ void fetch(uint32_t dst, uint32_t stride, const T* src, bool ok) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 16; ++i) cp_async16(dst + i * stride, src + i * (16 / sizeof(T)), ok);
+  }
+  static __device__ __forceinline__ void get(uint32_t src, uint32_t stride, float (&v)[8]) {
+    Vec8<T> t;
+    uint4 w[kBytes / 16];
+#pragma unroll
+    for (int i = 0; i < kBytes / 16; ++i) w[i] = lds16(src + i * stride);
+    memcpy(&t, w, sizeof(t));
+    t.get(v);
+  }
+};
+
 // ------------------------------------------------------------------ activations
 // sigmoid(z) = 1 / (1 + exp(-z)); exp(-z) = inf for z < -88 gives 0, as it should.
 __device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
@@ -107,7 +156,31 @@ __device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.0f, 1.
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-template <int ACT>
+// Phi(z) and phi(z), the normal distribution and its density, from one exponential:
+//   Phi(-a) = erfc(a / sqrt 2) / 2 = exp(-a^2 / 2) t Q(t) / 2,   t = 1 / (1 + 0.38 a / sqrt 2),
+// with Q the degree-6 polynomial whose largest relative error over 0 <= a / sqrt 2 <= 9.4 is
+// least (a Lawson-weighted least-squares fit of exp(x^2) erfc(x) / t): 1.0e-6, relative, in
+// the tail as well, against a half step of 4.9e-4 in fp16.  About 20 instructions where erff
+// and expf take about 60: with erff the backward pass was bound by arithmetic (217 us for
+// 8192 x 14336, 2.7 TB/s).
+__device__ __forceinline__ void normal_cdf(float z, float& cdf, float& density) {
+  const float a = fabsf(z);
+  const float t = __fdividef(1.0f, fmaf(0.38f * 0.7071067811865476f, a, 1.0f));
+  const float g = __expf(-0.5f * z * z);
+  float q = -0.12500557059902176f;
+  q = fmaf(q, t, 0.3344489817608761f);
+  q = fmaf(q, t, -0.06744702421290848f);
+  q = fmaf(q, t, 0.2458644792820478f);
+  q = fmaf(q, t, 0.18144377612944992f);
+  q = fmaf(q, t, 0.2163907947734426f);
+  q = fmaf(q, t, 0.21430355427606323f);
+  const float tail = 0.5f * q * t * g;
+  cdf = z < 0.0f ? tail : 1.0f - tail;
+  density = 0.3989422804014327f * g;
+}
+
+// EXACT: fp32 results (erff); otherwise results that are rounded to 16 bits.
+template <int ACT, bool EXACT = false>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == MAO_ACT_RELU) {
     return z < 0.0f ? 0.0f : z;  // a NaN stays one
@@ -115,7 +188,13 @@ __device__ __forceinline__ float act_value(float z) {
     const float r = z < 0.0f ? 0.0f : z;
     return r * r;
   } else if constexpr (ACT == MAO_ACT_GELU) {
-    return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    if constexpr (EXACT) {
+      return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    } else {
+      float c, d;
+      normal_cdf(z, c, d);
+      return z * c;
+    }
   } else if constexpr (ACT == MAO_ACT_GELU_TANH) {
     // (1 + tanh u) / 2 = sigmoid(2 u), without the cancellation of 1 + tanh u at u << 0
     return z * sigmoid_f(2.0f * kGeluA * (z + kGeluB * z * z * z));
@@ -133,8 +212,9 @@ __device__ __forceinline__ float act_slope(float z) {
   } else if constexpr (ACT == MAO_ACT_RELU2) {
     return 2.0f * (z < 0.0f ? 0.0f : z);
   } else if constexpr (ACT == MAO_ACT_GELU) {
-    // Phi(z) + z phi(z)
-    return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    float c, d;
+    normal_cdf(z, c, d);
+    return fmaf(z, d, c);  // Phi(z) + z phi(z)
   } else if constexpr (ACT == MAO_ACT_GELU_TANH) {
     // d/dz z s(v(z)) with v = 2 sqrt(2/pi) (z + b z^3): s + z s (1 - s) v'
     const float s = sigmoid_f(2.0f * kGeluA * (z + kGeluB * z * z * z));

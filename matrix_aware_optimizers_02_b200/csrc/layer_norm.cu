@@ -3,12 +3,16 @@
 // Both are HBM-bound, one pass over the activations: a row lives in the registers of the
 // G threads that own it (8 * VPT consecutive-by-8 columns each) from its load to its store.
 // Blocks walk rows with a stride, so a thread's columns stay the same: the weight and the
-// bias are read once per block, the next row's loads are issued before the present row's
-// reductions, and in the backward pass the column sums of dw and db accumulate in
-// registers, each block leaving one partial row for a second, small kernel.
+// bias are read once per block, and in the backward pass the column sums of dw and db
+// accumulate in registers, each block leaving one partial row for a second, small kernel.
+// A thread reads its share of the next rows ahead, by cp.async into a ring of its own in
+// shared memory: up to 200 KB in flight per SM, where the same loads held in registers, one
+// row ahead, left the passes waiting (backward 8191 x 1536 with residual: 49 us).
 //
 // Mean and variance: two passes over the registers (sum of x, then of (x - mean)^2), so
 // a large mean costs no digits.
+#include <atomic>
+
 #include "layer_host.h"
 
 namespace mao {
@@ -44,6 +48,25 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* sh) {
 template <int G>
 constexpr int kBlock = G < 128 ? 128 : G;
 
+// Stages of a thread's ring: as deep as kRingBytes of shared memory per SM allow at the
+// resident thread count, up to kMostStages; 0, plain loads into registers, where not one
+// fits (fp32 rows above 16384 columns).
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kMostStages = 4;
+constexpr int ring_stages(int bytes_per_thread, int resident) {
+  const int n = kRingBytes / (bytes_per_thread * resident);
+  return n > kMostStages ? kMostStages : n;
+}
+
+template <class T>
+__device__ __forceinline__ void load_vec(const T* p, long long ld, long long row, int c, int rows, int cols,
+                                         float (&v)[8]) {
+  Vec8<T> x;
+  if (row < rows && c < cols) x.load(p + row * ld + c);
+  else x.zero();
+  x.get(v);
+}
+
 // ------------------------------------------------------------------ forward
 struct FwdArgs {
   const void* x;
@@ -59,15 +82,42 @@ struct FwdArgs {
   float eps, inv_cols;
 };
 
+constexpr int kFwdThreads = 768;  // resident threads per SM that registers allow (blocks of 1024: one)
 template <class T, int G, int VPT>
-__global__ void __launch_bounds__(kBlock<G>) norm_kernel(const FwdArgs a) {
-  constexpr int B = kBlock<G>, R = B / G;  // rows per block at a time
+struct FwdCfg {
+  static constexpr int B = kBlock<G>;
+  static constexpr int kPerSm = B >= kFwdThreads ? 1 : kFwdThreads / B;
+  static constexpr int kStages = ring_stages(VPT * Slot8<T>::kBytes, kPerSm * B);
+  static constexpr int kSmem = kStages * VPT * Slot8<T>::kBytes * B;
+};
+
+template <class T, int G, int VPT>
+__global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_kernel(const FwdArgs a) {
+  using Cfg = FwdCfg<T, G, VPT>;
+  constexpr int B = Cfg::B, R = B / G;  // rows per block at a time
+  constexpr int D = Cfg::kStages;
+  constexpr uint32_t kVec = Slot8<T>::kBytes * B;  // one vector of every thread
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][32];
+  const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
   const int t = threadIdx.x % G;
   const int cols = a.cols;
   const T* x = static_cast<const T*>(a.x);
+  const long long step = (long long)gridDim.x * R;
+  const long long row0 = (long long)blockIdx.x * R + threadIdx.x / G;
+  auto fetch = [&](long long r, int stage) {
+    if constexpr (D == 0) return;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * G + t) * 8;
+      const bool ok = r < a.rows && c < cols;
+      Slot8<T>::fetch(slot0 + (stage * VPT + i) * kVec, B * 16, ok ? x + r * a.ld_x + c : x, ok);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) fetch(row0 + d * step, d);
   float w[VPT][8], b[VPT][8];
-  Vec8<T> next[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * G + t) * 8;
@@ -78,23 +128,20 @@ __global__ void __launch_bounds__(kBlock<G>) norm_kernel(const FwdArgs a) {
       if (a.b != nullptr) load_param8<T>(a.b, a.w_f32, c, b[i]);
     }
   }
-  const long long step = (long long)gridDim.x * R;
-  long long row = (long long)blockIdx.x * R + threadIdx.x / G;
-  auto fetch = [&](long long r) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * G + t) * 8;
-      if (r < a.rows && c < cols) next[i].load(x + r * a.ld_x + c);
-      else next[i].zero();
-    }
-  };
-  fetch(row);
+  long long row = row0;
+  int stage = 0;
   // the trip count is the block's: rows behind the last take part in the reductions
   for (long long r0 = (long long)blockIdx.x * R; r0 < a.rows; r0 += step, row += step) {
+    // the slot read in the iteration before is free: its values are in registers and used
+    fetch(row + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
+    if constexpr (D > 0) cp_async_wait<D - 1>();
     float v[VPT][8];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) next[i].get(v[i]);
-    fetch(row + step);
+    for (int i = 0; i < VPT; ++i) {
+      if constexpr (D > 0) Slot8<T>::get(slot0 + (stage * VPT + i) * kVec, B * 16, v[i]);
+      else load_vec(x, a.ld_x, row, (i * G + t) * 8, a.rows, cols, v[i]);
+    }
+    stage = stage >= D - 1 ? 0 : stage + 1;
     float s[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -139,6 +186,7 @@ __global__ void __launch_bounds__(kBlock<G>) norm_kernel(const FwdArgs a) {
       }
     }
   }
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ backward
@@ -150,7 +198,7 @@ struct BwdArgs {
   void* dx;
   const float* mean;
   const float* rstd;
-  float* part;  // [2][gridDim.x][cols]: partial sums of dw, then of db (each only if asked for)
+  float* part;  // [2][gridDim.x][cols]: partial sums of dw, then of db
   CkptView k;
   long long ld_dy, ld_x, ld_dres, ld_dx;
   int rows, cols;
@@ -158,34 +206,71 @@ struct BwdArgs {
   float inv_cols;
 };
 
-template <class T, bool KEPT>
-struct XVec {
-  Vec8<T> v;
-  __device__ __forceinline__ void load(const BwdArgs& a, long long r, int c) {
-    v.load(static_cast<const T*>(a.x) + r * a.ld_x + c);
-  }
-  __device__ __forceinline__ void zero() { v.zero(); }
-  __device__ __forceinline__ void get(float (&f)[8]) const { v.get(f); }
-};
-template <class T>
-struct XVec<T, true> {
-  CkptVec8 v;
-  __device__ __forceinline__ void load(const BwdArgs& a, long long r, int c) { v.load(a.k, r, c); }
-  __device__ __forceinline__ void zero() { v.zero(); }
-  __device__ __forceinline__ void get(float (&f)[8]) const { v.get(f); }
+constexpr int kBwdThreads = 512;  // resident threads per SM that registers allow (blocks of 1024: one)
+template <class T, bool KEPT, bool RES, int G, int VPT>
+struct BwdCfg {
+  static constexpr int B = kBlock<G>;
+  static constexpr int kPerSm = B >= kBwdThreads ? 1 : kBwdThreads / B;
+  static constexpr int kX = KEPT ? 8 : Slot8<T>::kBytes;  // bytes of x per vector
+  static constexpr int kVec = Slot8<T>::kBytes * (RES ? 2 : 1) + kX;
+  static constexpr int kStages = ring_stages(VPT * kVec, kPerSm * B);
+  static constexpr int kSmem = kStages * VPT * kVec * B;
 };
 
-template <class T, bool KEPT, int G, int VPT>
-__global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const BwdArgs a) {
-  constexpr int B = kBlock<G>, R = B / G;
+template <class T, bool KEPT, bool RES, int G, int VPT>
+__global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerSm) norm_bwd_kernel(const BwdArgs a) {
+  using Cfg = BwdCfg<T, KEPT, RES, G, VPT>;
+  constexpr int B = Cfg::B, R = B / G, D = Cfg::kStages;
+  constexpr uint32_t kT = Slot8<T>::kBytes * B;  // bytes of one vector of every thread
+  constexpr uint32_t kStage = Cfg::kVec * VPT * B;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][64];
+  const uint32_t base = smem_u32(ring);
   const int t = threadIdx.x % G;
   const int cols = a.cols;
   const T* dy = static_cast<const T*>(a.dy);
-  float w[VPT][8], dw[VPT][8], db[VPT][8];
-  Vec8<T> next_g[VPT];
-  XVec<T, KEPT> next_x[VPT];
+  const T* x = static_cast<const T*>(a.x);
+  const T* dres = static_cast<const T*>(a.dres);
+  const long long step = (long long)gridDim.x * R;
+  const long long row0 = (long long)blockIdx.x * R + threadIdx.x / G;
+  // a stage: VPT vectors of dy, then of dres, then of x
+  auto g_slot = [&](int stage, int i) { return base + stage * kStage + i * kT + threadIdx.x * 16; };
+  auto r_slot = [&](int stage, int i) { return base + stage * kStage + (VPT + i) * kT + threadIdx.x * 16; };
+  auto x_slot = [&](int stage, int i) {
+    return base + stage * kStage + (RES ? 2 : 1) * VPT * kT + i * (Cfg::kX * B) + threadIdx.x * (KEPT ? 8 : 16);
+  };
+  auto fetch = [&](long long r, int stage) {
+    if constexpr (D == 0) return;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * G + t) * 8;
+      const bool ok = r < a.rows && c < cols;
+      Slot8<T>::fetch(g_slot(stage, i), B * 16, ok ? dy + r * a.ld_dy + c : dy, ok);
+      if constexpr (KEPT) cp_async8(x_slot(stage, i), ok ? a.k.q + r * a.k.ld_q + c : a.k.q, ok);
+      else Slot8<T>::fetch(x_slot(stage, i), B * 16, ok ? x + r * a.ld_x + c : x, ok);
+      if constexpr (RES) Slot8<T>::fetch(r_slot(stage, i), B * 16, ok ? dres + r * a.ld_dres + c : dres, ok);
+    }
+    cp_async_commit();
+  };
+  // a row's statistics and its blocks' bytes come by plain loads, one row ahead
   float next_mean = 0.0f, next_rstd = 0.0f;
+  uint32_t next_e[VPT];
+  auto fetch_small = [&](long long r) {
+    const bool in = r < a.rows;
+    next_mean = in ? a.mean[r] : 0.0f;
+    next_rstd = in ? a.rstd[r] : 0.0f;
+    if constexpr (KEPT) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * G + t) * 8;
+        next_e[i] = (in && c < cols) ? a.k.e[r * a.k.ld_e + (c >> 5)] : 1u;
+      }
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) fetch(row0 + d * step, d);
+  fetch_small(row0);
+  float w[VPT][8], dw[VPT][8], db[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * G + t) * 8;
@@ -193,36 +278,38 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const BwdArgs a) {
     for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = db[i][j] = 0.0f;
     if (c < cols) load_param8<T>(a.w, a.w_f32, c, w[i]);
   }
-  const long long step = (long long)gridDim.x * R;
-  long long row = (long long)blockIdx.x * R + threadIdx.x / G;
-  auto fetch = [&](long long r) {
-    const bool in_rows = r < a.rows;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * G + t) * 8;
-      if (in_rows && c < cols) {
-        next_g[i].load(dy + r * a.ld_dy + c);
-        next_x[i].load(a, r, c);
-      } else {
-        next_g[i].zero();
-        next_x[i].zero();
-      }
-    }
-    next_mean = in_rows ? a.mean[r] : 0.0f;
-    next_rstd = in_rows ? a.rstd[r] : 0.0f;
-  };
-  fetch(row);
-  int buf = 0;
+  long long row = row0;
+  int stage = 0, buf = 0;
   for (long long r0 = (long long)blockIdx.x * R; r0 < a.rows; r0 += step, row += step, buf ^= 1) {
+    fetch(row + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
     const float mean = next_mean, rstd = next_rstd;
+    uint32_t e[VPT];
+    if constexpr (KEPT) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) e[i] = next_e[i];
+    }
+    fetch_small(row + step);
+    if constexpr (D > 0) cp_async_wait<D - 1>();
     const bool live = row < a.rows;
     float u[VPT][8], h[VPT][8];
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      const int c = (i * G + t) * 8;
+      if constexpr (D > 0) Slot8<T>::get(g_slot(stage, i), B * 16, u[i]);
+      else load_vec(dy, a.ld_dy, row, c, a.rows, cols, u[i]);
+      if constexpr (KEPT) {
+        CkptVec8 k;
+        if constexpr (D > 0) k.w = lds8(x_slot(stage, i));
+        else k.w = (live && c < cols) ? *reinterpret_cast<const uint2*>(a.k.q + row * a.k.ld_q + c) : make_uint2(0, 0);
+        k.e = e[i];
+        k.get(h[i]);
+      } else if constexpr (D > 0) {
+        Slot8<T>::get(x_slot(stage, i), B * 16, h[i]);
+      } else {
+        load_vec(x, a.ld_x, row, c, a.rows, cols, h[i]);
+      }
       const bool in = live && (i * G + t) * 8 < cols;
-      next_g[i].get(u[i]);
-      next_x[i].get(h[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         h[i][j] = in ? (h[i][j] - mean) * rstd : 0.0f;
@@ -233,16 +320,6 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const BwdArgs a) {
         s[1] = fmaf(u[i][j], h[i][j], s[1]);
       }
     }
-    Vec8<T> res[VPT];
-    if (a.dres != nullptr) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (i * G + t) * 8;
-        if (live && c < cols) res[i].load(static_cast<const T*>(a.dres) + row * a.ld_dres + c);
-        else res[i].zero();
-      }
-    }
-    fetch(row + step);
     row_sum<G, 2>(s, sh[buf]);
     const float mu = s[0] * a.inv_cols, mh = s[1] * a.inv_cols;
 #pragma unroll
@@ -251,9 +328,10 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const BwdArgs a) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = rstd * (u[i][j] - mu - h[i][j] * mh);
-      if (a.dres != nullptr) {
+      if constexpr (RES) {
         float r[8];
-        res[i].get(r);
+        if constexpr (D > 0) Slot8<T>::get(r_slot(stage, i), B * 16, r);
+        else load_vec(dres, a.ld_dres, row, c, a.rows, cols, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] += r[j];
       }
@@ -261,7 +339,9 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const BwdArgs a) {
       p.set(o);
       if (live && c < cols) p.store(static_cast<T*>(a.dx) + row * a.ld_dx + c);
     }
+    stage = stage >= D - 1 ? 0 : stage + 1;
   }
+  cp_async_wait<0>();
   if (a.part == nullptr) return;
   // the block's column sums: its R row groups joined in a fixed order
   float* pw = a.part + (long long)blockIdx.x * cols;
@@ -301,23 +381,32 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const BwdArgs a) {
 }
 
 // ------------------------------------------------------------------ column reduction
-// One warp-wide column strip per block: 32 columns x 8 lanes of parts, joined in a fixed
-// order, so the sums do not depend on how blocks are scheduled.
-__global__ void __launch_bounds__(256) col_reduce_kernel(const float* __restrict__ part, int parts, int cols,
-                                                         float* __restrict__ out) {
-  __shared__ float sh[8][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31);
-  const int g = threadIdx.x >> 5;
+// 32 columns per block, 32 warps over the parts, 4 loads in flight each; joined in a fixed
+// order, so the sums do not depend on how blocks are scheduled.  blockIdx.y picks one of two
+// sums whose parts lie one behind the other.
+__global__ void __launch_bounds__(1024) col_reduce_kernel(const float* __restrict__ part, int parts, int cols,
+                                                          float* __restrict__ out0, float* __restrict__ out1) {
+  __shared__ float sh[32][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float* out = blockIdx.y == 0 ? out0 : out1;
+  if (out == nullptr) return;
+  const float* p = part + (long long)blockIdx.y * parts * cols + c;
   float s = 0.0f;
-  if (c < cols)
-    for (int p = g; p < parts; p += 8) s += part[(long long)p * cols + c];
-  sh[g][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (g == 0 && c < cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
-    out[c] = s;
+  if (c < cols) {
+    int i = g;
+    for (; i + 96 < parts; i += 128) {
+      const float v0 = p[(long long)i * cols], v1 = p[(long long)(i + 32) * cols], v2 = p[(long long)(i + 64) * cols],
+                  v3 = p[(long long)(i + 96) * cols];
+      s += (v0 + v1) + (v2 + v3);
+    }
+    for (; i < parts; i += 32) s += p[(long long)i * cols];
   }
+  sh[g][lane] = s;
+  __syncthreads();
+  // warp g sums column g of the strip: lane by lane, then by shuffles in a fixed tree
+  s = warp_sum(sh[lane][g]);
+  if (lane == 0 && blockIdx.x * 32 + g < cols) out[blockIdx.x * 32 + g] = s;
 }
 
 // ------------------------------------------------------------------ dispatch
@@ -335,49 +424,74 @@ __global__ void __launch_bounds__(256) col_reduce_kernel(const float* __restrict
 
 // Blocks of a walk over `rows`: as many as are resident at once, never more than there is
 // work for.  The backward pass writes 8 * cols bytes of partial sums per block.
-int threads_of(int cols) {
-  int b = 0;
-#define MAO_CASE(G, V) b = kBlock<G>;
+int walk_blocks(int rows, int rows_at_a_time, int per_sm, int sm_count) {
+  return std::min((rows + rows_at_a_time - 1) / rows_at_a_time, per_sm * sm_count);
+}
+constexpr int kSizingSms = 160;  // at least the SMs of any sm_100 part, for workspace sizes
+
+int bwd_blocks(int rows, int cols, int sms) {
+  int n = 0;
+#define MAO_CASE(G, V) n = walk_blocks(rows, kBlock<G> / G, kBlock<G> >= kBwdThreads ? 1 : kBwdThreads / kBlock<G>, sms);
   MAO_NORM_SIZES(MAO_CASE)
 #undef MAO_CASE
-  return b;
+  return n;
 }
-int rows_per_block(int cols) {
-  int r = 0;
-#define MAO_CASE(G, V) r = kBlock<G> / G;
-  MAO_NORM_SIZES(MAO_CASE)
-#undef MAO_CASE
-  return r;
+
+// A kernel's dynamic shared memory limit, raised once per device.
+template <class K>
+mao_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
+  int d = 0;
+  MAO_CUDA_TRY(cudaGetDevice(&d));  // device_info has bounded it
+  if (!done[d].load(std::memory_order_acquire)) {
+    MAO_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done[d].store(true, std::memory_order_release);
+  }
+  return MAO_OK;
 }
-int walk_blocks(int rows, int cols, int sm_count, int threads_per_sm) {
-  const int per_sm = std::max(1, threads_per_sm / threads_of(cols));
-  const int rpb = rows_per_block(cols);
-  return std::min((rows + rpb - 1) / rpb, per_sm * sm_count);
+
+template <class T, int G, int VPT>
+mao_status fwd_one(const FwdArgs& a, int sms, cudaStream_t stream) {
+  using Cfg = FwdCfg<T, G, VPT>;
+  static std::atomic<bool> done[64];
+  MAO_TRY(allow_smem(norm_kernel<T, G, VPT>, Cfg::kSmem, done));
+  const int grid = walk_blocks(a.rows, Cfg::B / G, Cfg::kPerSm, sms);
+  norm_kernel<T, G, VPT><<<grid, Cfg::B, Cfg::kSmem, stream>>>(a);
+  return launched();
 }
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;  // resident threads per SM that registers allow
-constexpr int kSizingSms = 160;                       // at least the SMs of any sm_100 part, for workspace sizes
 
 template <class T>
 mao_status fwd(const FwdArgs& a, int sms, cudaStream_t stream) {
   const int cols = a.cols;
-  const int grid = walk_blocks(a.rows, cols, sms, kFwdThreads);
   LaunchScope ls(stream, MAO_K_LAYER_NORM, 0.0,
                  (double)a.rows * cols * (2.0 * sizeof(T) + (a.k.q ? 1.0 + 1.0 / 32 : 0.0)));
-#define MAO_CASE(G, V) norm_kernel<T, G, V><<<grid, kBlock<G>, 0, stream>>>(a);
+#define MAO_CASE(G, V) return fwd_one<T, G, V>(a, sms, stream);
   MAO_NORM_SIZES(MAO_CASE)
 #undef MAO_CASE
+}
+
+template <class T, bool KEPT, bool RES, int G, int VPT>
+mao_status bwd_one(const BwdArgs& a, int grid, cudaStream_t stream) {
+  using Cfg = BwdCfg<T, KEPT, RES, G, VPT>;
+  static std::atomic<bool> done[64];
+  MAO_TRY(allow_smem(norm_bwd_kernel<T, KEPT, RES, G, VPT>, Cfg::kSmem, done));
+  norm_bwd_kernel<T, KEPT, RES, G, VPT><<<grid, Cfg::B, Cfg::kSmem, stream>>>(a);
   return launched();
 }
 
-template <class T, bool KEPT>
-mao_status bwd(const BwdArgs& a, int grid, cudaStream_t stream) {
+template <class T, bool KEPT, bool RES>
+mao_status bwd_sized(const BwdArgs& a, int grid, cudaStream_t stream) {
   const int cols = a.cols;
   LaunchScope ls(stream, MAO_K_LAYER_NORM_BWD, 0.0,
-                 (double)a.rows * cols * (2.0 * sizeof(T) + (KEPT ? 1.0 + 1.0 / 32 : sizeof(T)) + (a.dres ? sizeof(T) : 0)));
-#define MAO_CASE(G, V) norm_bwd_kernel<T, KEPT, G, V><<<grid, kBlock<G>, 0, stream>>>(a);
+                 (double)a.rows * cols * ((RES ? 3.0 : 2.0) * sizeof(T) + (KEPT ? 1.0 + 1.0 / 32 : sizeof(T))));
+#define MAO_CASE(G, V) return bwd_one<T, KEPT, RES, G, V>(a, grid, stream);
   MAO_NORM_SIZES(MAO_CASE)
 #undef MAO_CASE
-  return launched();
+}
+
+template <class T>
+mao_status bwd(const BwdArgs& a, bool kept, int grid, cudaStream_t stream) {
+  if (kept) return a.dres ? bwd_sized<T, true, true>(a, grid, stream) : bwd_sized<T, true, false>(a, grid, stream);
+  return a.dres ? bwd_sized<T, false, true>(a, grid, stream) : bwd_sized<T, false, false>(a, grid, stream);
 }
 
 mao_status check_w(int w_dtype, int dtype) {
@@ -395,14 +509,14 @@ mao_status check_bwd(const mao_layer_norm_backward_args* a) {
 
 size_t bwd_bytes(const mao_layer_norm_backward_args* a, int sms) {
   if (a->dw == nullptr && a->db == nullptr) return 0;
-  return sizeof(float) * 2 * (size_t)walk_blocks(a->rows, a->cols, sms, kBwdThreads) * (size_t)a->cols;
+  return sizeof(float) * 2 * (size_t)bwd_blocks(a->rows, a->cols, sms) * (size_t)a->cols;
 }
 
 }  // namespace
 
-mao_status col_reduce_launch(const float* part, int parts, int cols, float* out, cudaStream_t stream) {
-  LaunchScope ls(stream, MAO_K_COL_REDUCE, 0.0, 4.0 * (double)parts * cols);
-  col_reduce_kernel<<<(cols + 31) / 32, 256, 0, stream>>>(part, parts, cols, out);
+mao_status col_reduce_launch(const float* part, int parts, int cols, float* out0, float* out1, cudaStream_t stream) {
+  LaunchScope ls(stream, MAO_K_COL_REDUCE, 0.0, 4.0 * (double)parts * cols * (out1 ? 2 : 1));
+  col_reduce_kernel<<<dim3((cols + 31) / 32, out1 ? 2 : 1), 1024, 0, stream>>>(part, parts, cols, out0, out1);
   return launched();
 }
 
@@ -486,17 +600,14 @@ extern "C" mao_status mao_layer_norm_backward(const mao_layer_norm_backward_args
   g.rows = a->rows, g.cols = a->cols;
   g.w_f32 = a->w_dtype == MAO_F32;
   g.inv_cols = 1.0f / (float)a->cols;
-  const int grid = walk_blocks(a->rows, a->cols, dev->sm_count, kBwdThreads);
+  const int grid = bwd_blocks(a->rows, a->cols, dev->sm_count);
   mao_status st;
   switch (a->dtype) {
-    case MAO_F32: st = kept ? bwd<float, true>(g, grid, stream) : bwd<float, false>(g, grid, stream); break;
-    case MAO_BF16:
-      st = kept ? bwd<__nv_bfloat16, true>(g, grid, stream) : bwd<__nv_bfloat16, false>(g, grid, stream);
-      break;
-    default: st = kept ? bwd<__half, true>(g, grid, stream) : bwd<__half, false>(g, grid, stream); break;
+    case MAO_F32: st = bwd<float>(g, kept, grid, stream); break;
+    case MAO_BF16: st = bwd<__nv_bfloat16>(g, kept, grid, stream); break;
+    default: st = bwd<__half>(g, kept, grid, stream); break;
   }
   if (st != MAO_OK) return st;
-  if (a->dw) MAO_TRY(col_reduce_launch(g.part, grid, a->cols, a->dw, stream));
-  if (a->db) MAO_TRY(col_reduce_launch(g.part + (size_t)grid * a->cols, grid, a->cols, a->db, stream));
-  return MAO_OK;
+  if (a->dw == nullptr && a->db == nullptr) return MAO_OK;
+  return col_reduce_launch(g.part, grid, a->cols, a->dw, a->db, stream);
 }

@@ -182,7 +182,7 @@ mao_status backward(const mao_linear_backward_args* a, const BwdLayout& L, uint8
     if (out) dz = out, ld_dz = a->m;
     if (a->db) {
       const int chunk = act_bwd_chunk(a->rows, a->m);
-      MAO_TRY(col_reduce_launch(part, (a->rows + chunk - 1) / chunk, a->m, a->db, stream));
+      MAO_TRY(col_reduce_launch(part, (a->rows + chunk - 1) / chunk, a->m, a->db, nullptr, stream));
     }
   }
   float* part = reinterpret_cast<float*>(ws + L.part);
