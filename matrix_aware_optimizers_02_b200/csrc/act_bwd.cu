@@ -23,13 +23,13 @@ constexpr int kRowsInFlight = 4;
 
 template <class T, int ACT, bool KEPT>
 __global__ void __launch_bounds__(256) act_bwd_kernel(const ActArgs a) {
-  __shared__ float sh[8][256];
+  __shared__ float2 sh[8][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * 8;
   const long long r_end = min((long long)a.rows, ((long long)blockIdx.y + 1) * a.chunk);
-  float sum[8];
+  f2 sum[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  for (int j = 0; j < 4; ++j) sum[j] = dup2(0.0f);
   if (c < a.cols) {
     for (long long r0 = (long long)blockIdx.y * a.chunk + warp; r0 < r_end; r0 += 8 * kRowsInFlight) {
       Vec8<T> g[kRowsInFlight];
@@ -50,31 +50,32 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const ActArgs a) {
       for (int i = 0; i < kRowsInFlight; ++i) {
         const long long r = r0 + 8 * i;
         if (r < r_end) {
-          float d[8];
+          f2 d[4];
           g[i].get(d);
           if constexpr (ACT != MAO_ACT_NONE) {
-            float f[8];
+            f2 f[4];
             if constexpr (KEPT) zk[i].get(f);
             else z[i].get(f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] *= act_slope<ACT>(f[j]);
+            for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], act_slope<ACT>(f[j]));
             Vec8<T> o;
             o.set(d);
             if (a.dz != nullptr) o.store(static_cast<T*>(a.dz) + r * a.ld_dz + c);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sum[j] += d[j];
+          for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], d[j]);
         }
       }
     }
   }
   if (a.part == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sh[warp][lane * 8 + j] = sum[j];
+  for (int j = 0; j < 4; ++j) sh[warp][lane * 4 + j] = sum[j];
   __syncthreads();
+  const float* p = reinterpret_cast<const float*>(sh);
   float s = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) s += sh[w][threadIdx.x];
+  for (int w = 0; w < 8; ++w) s += p[w * 256 + threadIdx.x];
   const int col = blockIdx.x * 256 + threadIdx.x;
   if (col < a.cols) a.part[(long long)blockIdx.y * a.cols + col] = s;
 }

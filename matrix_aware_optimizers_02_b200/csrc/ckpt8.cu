@@ -12,108 +12,129 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 
-// Vector index -> (row, column).  `vpr` vectors per row, rows padded to whole blocks.
-struct Split {
+// A thread's walk over vectors of 8, `stride` = gridDim.x * kThreads apart: one division at its
+// start, then additions (dr rows and dv vectors per step; a division per vector made the read
+// back issue-bound: 133 instructions per vector).
+struct Walk {
   long long row;
-  int col;
-  __device__ __forceinline__ Split(long long i, int vpr) {
-    if (i < (1ll << 32)) {
-      const uint32_t r = (uint32_t)i / (uint32_t)vpr;
-      row = r;
-      col = ((uint32_t)i - r * (uint32_t)vpr) * 8;
-    } else {
-      row = i / vpr;
-      col = (int)(i - row * vpr) * 8;
-    }
+  int v;
+  __device__ __forceinline__ Walk(int vpr) {
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;  // below 2^31
+    row = (uint32_t)i / (uint32_t)vpr;
+    v = (int)((uint32_t)i - (uint32_t)row * (uint32_t)vpr);
   }
+  __device__ __forceinline__ void next(int dr, int dv, int vpr) {
+    row += dr;
+    v += dv;
+    if (v >= vpr) v -= vpr, ++row;
+  }
+};
+struct Steps {
+  long long total;  // vectors
+  int rows, vpr, dr, dv;
 };
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x, long long ld_x, CkptView k,
-                                                         long long total, int vpr, int cols) {
-  const long long base = (long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  Vec8<T> v[kUnroll];
+__global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x, long long ld_x, CkptView k, Steps st,
+                                                         int cols) {
+  Walk at(st.vpr);
+  const long long stride = (long long)gridDim.x * kThreads;
+  // uniform over the block: lanes behind the last vector take part in the shuffles
+  for (long long i = (long long)blockIdx.x * kThreads; i < st.total; i += kUnroll * stride) {
+    Vec8<T> v[kUnroll];
+    long long row[kUnroll];
+    int col[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const long long i = base + u * kThreads;
-    v[u].zero();
-    if (i < total) {
-      const Split s(i, vpr);
-      if (s.col < cols) v[u].load(x + s.row * ld_x + s.col);
+    for (int u = 0; u < kUnroll; ++u) {
+      row[u] = at.row;
+      col[u] = at.v * 8;
+      if (at.row < st.rows && col[u] < cols) v[u].load(x + at.row * ld_x + col[u]);
+      else v[u].zero();
+      at.next(st.dr, st.dv, st.vpr);
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const long long i = base + u * kThreads;
-    const Split s(i < total ? i : 0, vpr);
-    float f[8];
-    v[u].get(f);
-    ckpt_store8(k, s.row, s.col, f, i < total);  // 4 | vpr: a block's lanes are all in or all out
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t amax = v[u].block_max();  // 4 | vpr: a block's lanes are all in or all out
+      f2 f[4];
+      v[u].get(f);
+      if (row[u] < st.rows) ckpt_store8(k, row[u], col[u], f, amax);
+    }
   }
 }
 
 template <class T, int ACT>
-__global__ void __launch_bounds__(kThreads) restore_kernel(CkptView k, T* __restrict__ y, long long ld_y,
-                                                           long long total, int vpr) {
-  const long long base = (long long)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  CkptVec8 v[kUnroll];
+__global__ void __launch_bounds__(kThreads) restore_kernel(CkptView k, T* __restrict__ y, long long ld_y, Steps st) {
+  Walk at(st.vpr);
+  while (at.row < st.rows) {
+    CkptVec8 v[kUnroll];
+    long long row[kUnroll];
+    int col[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const long long i = base + u * kThreads;
-    if (i < total) {
-      const Split s(i, vpr);
-      v[u].load(k, s.row, s.col);
+    for (int u = 0; u < kUnroll; ++u) {
+      row[u] = at.row;
+      col[u] = at.v * 8;
+      if (at.row < st.rows) v[u].load(k, at.row, col[u]);
+      at.next(st.dr, st.dv, st.vpr);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (row[u] >= st.rows) break;
+      f2 f[4];
+      v[u].get(f);
+      Vec8<T> o;
+      if constexpr (ACT == MAO_ACT_NONE) {
+        o.set_exact(f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = act_value<ACT, sizeof(T) == 4>(f[j]);
+        o.set(f);
+      }
+      o.store(y + row[u] * ld_y + col[u]);
     }
   }
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const long long i = base + u * kThreads;
-    if (i >= total) continue;
-    const Split s(i, vpr);
-    float f[8];
-    v[u].get(f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = act_value<ACT, sizeof(T) == 4>(f[j]);
-    Vec8<T> o;
-    o.set(f);
-    o.store(y + s.row * ld_y + s.col);
-  }
 }
 
-bool grid_of(long long total, unsigned* grid) {
-  const long long g = (total + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  *grid = (unsigned)g;
-  return g <= INT_MAX;
+// One wave of blocks walks everything; never more blocks than vectors ask for.
+unsigned steps_of(int rows, int vpr, int sms, Steps* s) {
+  s->total = (long long)rows * vpr;
+  s->rows = rows;
+  s->vpr = vpr;
+  const long long want = (s->total + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+  const long long grid = std::min<long long>(want, 8ll * sms);
+  s->dr = (int)(grid * kThreads / vpr);
+  s->dv = (int)(grid * kThreads % vpr);
+  return (unsigned)grid;
 }
-
 template <class T>
 mao_status pack(const void* x, long long ld_x, const CkptView& k, int rows, int cols, cudaStream_t stream) {
   const int vpr = ckpt_blocks(cols) * 4;
-  const long long total = (long long)rows * vpr;
-  unsigned grid;
-  if (!grid_of(total, &grid)) return MAO_ERR_SHAPE;
+  DeviceInfo* dev = nullptr;
+  MAO_TRY(device_info(&dev));
+  Steps st;
+  const unsigned grid = steps_of(rows, vpr, dev->sm_count, &st);
   LaunchScope ls(stream, MAO_K_CKPT8, 0.0, (double)rows * cols * (sizeof(T) + 1.0 + 1.0 / 32));
-  ckpt8_kernel<T><<<grid, kThreads, 0, stream>>>(static_cast<const T*>(x), ld_x, k, total, vpr, cols);
+  ckpt8_kernel<T><<<grid, kThreads, 0, stream>>>(static_cast<const T*>(x), ld_x, k, st, cols);
   return launched();
 }
 
 template <class T>
 mao_status restore(const CkptView& k, int rows, int cols, int act, void* y, long long ld_y, cudaStream_t stream) {
   const int vpr = cols / 8;
-  const long long total = (long long)rows * vpr;
-  unsigned grid;
-  if (!grid_of(total, &grid)) return MAO_ERR_SHAPE;
+  DeviceInfo* dev = nullptr;
+  MAO_TRY(device_info(&dev));
+  Steps st;
+  const unsigned grid = steps_of(rows, vpr, dev->sm_count, &st);
   T* o = static_cast<T*>(y);
   LaunchScope ls(stream, MAO_K_CKPT8_RESTORE, 0.0, (double)rows * cols * (sizeof(T) + 1.0 + 1.0 / 32));
   switch (act) {
-    case MAO_ACT_NONE: restore_kernel<T, MAO_ACT_NONE><<<grid, kThreads, 0, stream>>>(k, o, ld_y, total, vpr); break;
-    case MAO_ACT_RELU: restore_kernel<T, MAO_ACT_RELU><<<grid, kThreads, 0, stream>>>(k, o, ld_y, total, vpr); break;
-    case MAO_ACT_RELU2: restore_kernel<T, MAO_ACT_RELU2><<<grid, kThreads, 0, stream>>>(k, o, ld_y, total, vpr); break;
-    case MAO_ACT_GELU: restore_kernel<T, MAO_ACT_GELU><<<grid, kThreads, 0, stream>>>(k, o, ld_y, total, vpr); break;
+    case MAO_ACT_NONE: restore_kernel<T, MAO_ACT_NONE><<<grid, kThreads, 0, stream>>>(k, o, ld_y, st); break;
+    case MAO_ACT_RELU: restore_kernel<T, MAO_ACT_RELU><<<grid, kThreads, 0, stream>>>(k, o, ld_y, st); break;
+    case MAO_ACT_RELU2: restore_kernel<T, MAO_ACT_RELU2><<<grid, kThreads, 0, stream>>>(k, o, ld_y, st); break;
+    case MAO_ACT_GELU: restore_kernel<T, MAO_ACT_GELU><<<grid, kThreads, 0, stream>>>(k, o, ld_y, st); break;
     case MAO_ACT_GELU_TANH:
-      restore_kernel<T, MAO_ACT_GELU_TANH><<<grid, kThreads, 0, stream>>>(k, o, ld_y, total, vpr);
+      restore_kernel<T, MAO_ACT_GELU_TANH><<<grid, kThreads, 0, stream>>>(k, o, ld_y, st);
       break;
-    case MAO_ACT_SILU: restore_kernel<T, MAO_ACT_SILU><<<grid, kThreads, 0, stream>>>(k, o, ld_y, total, vpr); break;
+    case MAO_ACT_SILU: restore_kernel<T, MAO_ACT_SILU><<<grid, kThreads, 0, stream>>>(k, o, ld_y, st); break;
     default: return MAO_ERR_INVALID_ARG;
   }
   return launched();

@@ -35,13 +35,12 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* sh) {
       for (int i = 0; i < N; ++i) sh[warp * N + i] = v[i];
     }
     __syncthreads();
-    const float* r = sh + (warp / W) * W * N;
+    const float2* r = reinterpret_cast<const float2*>(sh + (warp / W) * W * N);
+    f2 p = dup2(0.0f);  // N = 1: even and odd warps; N = 2: the two sums
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += r[w * N + i];
+    for (int w = 0; w < W * N / 2; ++w) p = add2(p, r[w]);
+    if constexpr (N == 1) v[0] = p.x + p.y;
+    else v[0] = p.x, v[1] = p.y;
   }
 }
 
@@ -60,11 +59,9 @@ constexpr int ring_stages(int bytes_per_thread, int resident) {
 
 template <class T>
 __device__ __forceinline__ void load_vec(const T* p, long long ld, long long row, int c, int rows, int cols,
-                                         float (&v)[8]) {
-  Vec8<T> x;
+                                         Vec8<T>& x) {
   if (row < rows && c < cols) x.load(p + row * ld + c);
   else x.zero();
-  x.get(v);
 }
 
 // ------------------------------------------------------------------ forward
@@ -98,7 +95,7 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
   constexpr int D = Cfg::kStages;
   constexpr uint32_t kVec = Slot8<T>::kBytes * B;  // one vector of every thread
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float sh[2][32];
+  __shared__ __align__(16) float sh[2][32];
   const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
   const int t = threadIdx.x % G;
   const int cols = a.cols;
@@ -117,12 +114,12 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
   };
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) fetch(row0 + d * step, d);
-  float w[VPT][8], b[VPT][8];
+  f2 w[VPT][4], b[VPT][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * G + t) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = b[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) w[i][j] = b[i][j] = dup2(0.0f);
     if (c < cols) {
       load_param8<T>(a.w, a.w_f32, c, w[i]);
       if (a.b != nullptr) load_param8<T>(a.b, a.w_f32, c, b[i]);
@@ -135,30 +132,34 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
     // the slot read in the iteration before is free: its values are in registers and used
     fetch(row + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
     if constexpr (D > 0) cp_async_wait<D - 1>();
-    float v[VPT][8];
+    f2 v[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if constexpr (D > 0) Slot8<T>::get(slot0 + (stage * VPT + i) * kVec, B * 16, v[i]);
-      else load_vec(x, a.ld_x, row, (i * G + t) * 8, a.rows, cols, v[i]);
+      Vec8<T> p;
+      if constexpr (D > 0) p = Slot8<T>::get(slot0 + (stage * VPT + i) * kVec, B * 16);
+      else load_vec(x, a.ld_x, row, (i * G + t) * 8, a.rows, cols, p);
+      p.get(v[i]);
     }
     stage = stage >= D - 1 ? 0 : stage + 1;
-    float s[1] = {0.0f};
+    f2 p = dup2(0.0f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += v[i][j];
+      for (int j = 0; j < 4; ++j) p = add2(p, v[i][j]);
+    float s[1] = {p.x + p.y};
     row_sum<G, 1>(s, sh[0]);
     const float mean = s[0] * a.inv_cols;
-    s[0] = 0.0f;
+    p = dup2(0.0f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const bool in = (i * G + t) * 8 < cols;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] -= mean;
-        if (in) s[0] = fmaf(v[i][j], v[i][j], s[0]);
+      for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], dup2(-mean));
+      if ((i * G + t) * 8 < cols) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p = fma2(v[i][j], v[i][j], p);
       }
     }
+    s[0] = p.x + p.y;
     row_sum<G, 1>(s, sh[1]);
     const float rstd = 1.0f / sqrtf(s[0] * a.inv_cols + a.eps);
     const bool live = row < a.rows;
@@ -169,20 +170,19 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * G + t) * 8;
-      float o[8];
+      const bool in = live && c < cols;
+      f2 o[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = fmaf(v[i][j] * rstd, w[i][j], b[i][j]);
-      Vec8<T> p;
-      p.set(o);
-      if (live && c < cols) p.store(static_cast<T*>(a.y) + row * a.ld_y + c);
+      for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], dup2(rstd)), w[i][j], b[i][j]);
+      Vec8<T> q;
+      q.set(o);
+      if (in) q.store(static_cast<T*>(a.y) + row * a.ld_y + c);
       if (a.k.q != nullptr) {
         // the checkpoint is of y as stored; lanes behind the last column hold zeros
-        p.get(o);
-        if (c >= cols) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-        }
-        ckpt_store8(a.k, row, c, o, live && (c & ~31) < cols);
+        if (c >= cols) q.zero();
+        const uint32_t amax = q.block_max();
+        q.get(o);
+        if (live && (c & ~31) < cols) ckpt_store8(a.k, row, c, o, amax);
       }
     }
   }
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
   constexpr uint32_t kT = Slot8<T>::kBytes * B;  // bytes of one vector of every thread
   constexpr uint32_t kStage = Cfg::kVec * VPT * B;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float sh[2][64];
+  __shared__ __align__(16) float sh[2][64];
   const uint32_t base = smem_u32(ring);
   const int t = threadIdx.x % G;
   const int cols = a.cols;
@@ -252,88 +252,99 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
     }
     cp_async_commit();
   };
-  // a row's statistics and its blocks' bytes come by plain loads, one row ahead
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  uint32_t next_e[VPT];
+  // a row's statistics and its blocks' bytes come by plain loads into registers, two rows
+  // ahead (one row ahead the loop waited for them)
+  struct Small {
+    float mean, rstd;
+    uint32_t e[VPT];
+  };
   auto fetch_small = [&](long long r) {
+    Small q;
     const bool in = r < a.rows;
-    next_mean = in ? a.mean[r] : 0.0f;
-    next_rstd = in ? a.rstd[r] : 0.0f;
+    q.mean = in ? a.mean[r] : 0.0f;
+    q.rstd = in ? a.rstd[r] : 0.0f;
     if constexpr (KEPT) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = (i * G + t) * 8;
-        next_e[i] = (in && c < cols) ? a.k.e[r * a.k.ld_e + (c >> 5)] : 1u;
+        q.e[i] = (in && c < cols) ? a.k.e[r * a.k.ld_e + (c >> 5)] : 1u;
       }
     }
+    return q;
   };
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) fetch(row0 + d * step, d);
-  fetch_small(row0);
-  float w[VPT][8], dw[VPT][8], db[VPT][8];
+  Small now, next = fetch_small(row0), after = fetch_small(row0 + step);
+  f2 w[VPT][4], dw[VPT][4], db[VPT][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * G + t) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = db[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) w[i][j] = dw[i][j] = db[i][j] = dup2(0.0f);
     if (c < cols) load_param8<T>(a.w, a.w_f32, c, w[i]);
   }
   long long row = row0;
   int stage = 0, buf = 0;
   for (long long r0 = (long long)blockIdx.x * R; r0 < a.rows; r0 += step, row += step, buf ^= 1) {
     fetch(row + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
-    const float mean = next_mean, rstd = next_rstd;
-    uint32_t e[VPT];
-    if constexpr (KEPT) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) e[i] = next_e[i];
-    }
-    fetch_small(row + step);
+    now = next;
+    next = after;
+    after = fetch_small(row + 2 * step);
     if constexpr (D > 0) cp_async_wait<D - 1>();
     const bool live = row < a.rows;
-    float u[VPT][8], h[VPT][8];
-    float s[2] = {0.0f, 0.0f};
+    // where nothing is to be read (columns and rows behind the last) dy is 0, so u and every
+    // sum's term are 0
+    f2 u[VPT][4], h[VPT][4];
+    f2 s0 = dup2(0.0f), s1 = dup2(0.0f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * G + t) * 8;
-      if constexpr (D > 0) Slot8<T>::get(g_slot(stage, i), B * 16, u[i]);
-      else load_vec(dy, a.ld_dy, row, c, a.rows, cols, u[i]);
+      Vec8<T> p;
+      if constexpr (D > 0) p = Slot8<T>::get(g_slot(stage, i), B * 16);
+      else load_vec(dy, a.ld_dy, row, c, a.rows, cols, p);
+      p.get(u[i]);
       if constexpr (KEPT) {
         CkptVec8 k;
         if constexpr (D > 0) k.w = lds8(x_slot(stage, i));
         else k.w = (live && c < cols) ? *reinterpret_cast<const uint2*>(a.k.q + row * a.k.ld_q + c) : make_uint2(0, 0);
-        k.e = e[i];
+        k.e = now.e[i];
         k.get(h[i]);
-      } else if constexpr (D > 0) {
-        Slot8<T>::get(x_slot(stage, i), B * 16, h[i]);
       } else {
-        load_vec(x, a.ld_x, row, c, a.rows, cols, h[i]);
+        if constexpr (D > 0) p = Slot8<T>::get(x_slot(stage, i), B * 16);
+        else load_vec(x, a.ld_x, row, c, a.rows, cols, p);
+        p.get(h[i]);
       }
-      const bool in = live && (i * G + t) * 8 < cols;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[i][j] = in ? (h[i][j] - mean) * rstd : 0.0f;
-        dw[i][j] = fmaf(u[i][j], h[i][j], dw[i][j]);
-        db[i][j] += u[i][j];
-        u[i][j] *= w[i][j];
-        s[0] += u[i][j];
-        s[1] = fmaf(u[i][j], h[i][j], s[1]);
+      for (int j = 0; j < 4; ++j) {
+        h[i][j] = mul2(add2(h[i][j], dup2(-now.mean)), dup2(now.rstd));
+        dw[i][j] = fma2(u[i][j], h[i][j], dw[i][j]);
+        db[i][j] = add2(db[i][j], u[i][j]);
+        u[i][j] = mul2(u[i][j], w[i][j]);
+        s0 = add2(s0, u[i][j]);
+        s1 = fma2(u[i][j], h[i][j], s1);
       }
     }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};
     row_sum<G, 2>(s, sh[buf]);
-    const float mu = s[0] * a.inv_cols, mh = s[1] * a.inv_cols;
+    // rstd (u - mean(u) - h mean(u h))
+    const f2 mu = dup2(-s[0] * a.inv_cols), mh = dup2(-s[1] * a.inv_cols);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * G + t) * 8;
-      float o[8];
+      f2 o[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = rstd * (u[i][j] - mu - h[i][j] * mh);
+      for (int j = 0; j < 4; ++j) o[j] = fma2(h[i][j], mh, add2(u[i][j], mu));
       if constexpr (RES) {
-        float r[8];
-        if constexpr (D > 0) Slot8<T>::get(r_slot(stage, i), B * 16, r);
-        else load_vec(dres, a.ld_dres, row, c, a.rows, cols, r);
+        Vec8<T> p;
+        if constexpr (D > 0) p = Slot8<T>::get(r_slot(stage, i), B * 16);
+        else load_vec(dres, a.ld_dres, row, c, a.rows, cols, p);
+        f2 r[4];
+        p.get(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += r[j];
+        for (int j = 0; j < 4; ++j) o[j] = fma2(o[j], dup2(now.rstd), r[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = mul2(o[j], dup2(now.rstd));
       }
       Vec8<T> p;
       p.set(o);
@@ -359,14 +370,15 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
       }
     }
   } else {
-    __shared__ float acc[R][G * 8];
+    __shared__ __align__(16) float acc[R][G * 8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[threadIdx.x / G][t * 8 + j] = which ? db[i][j] : dw[i][j];
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<f2*>(&acc[threadIdx.x / G][t * 8 + 2 * j]) = which ? db[i][j] : dw[i][j];
         __syncthreads();
         for (int e = threadIdx.x; e < G * 8; e += B) {
           float sum = 0.0f;

@@ -73,7 +73,10 @@ struct LinParams {
 template <int ACT>
 __device__ __forceinline__ void act32(float* v) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = act_value<ACT>(v[j]);
+  for (int j = 0; j < 32; j += 2) {
+    const f2 r = act_value<ACT>(make_float2(v[j], v[j + 1]));
+    v[j] = r.x, v[j + 1] = r.y;
+  }
 }
 
 // 32 consecutive 16-bit elements of one row, `n` of them valid (a multiple of 8)
@@ -122,25 +125,25 @@ __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int 
 #pragma unroll
       for (int j = 0; j < 32; j += 8)
         if (j < n) {
-          float b[8];
+          f2 b[4];
           load_param8<T>(e.bias, e.bias_f32, col + j, b);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[j + i] += b[i];
+          for (int i = 0; i < 4; ++i) v[j + 2 * i] += b[i].x, v[j + 2 * i + 1] += b[i].y;
         }
     }
     if (e.z != nullptr) store16x32<T>(static_cast<T*>(e.z) + (long long)row * e.ld_z + col, v, n);
     if (e.k.q != nullptr) {
       // this thread's 32 columns are one block of the checkpoint; columns behind the last
       // hold zeros (the operands' out-of-range rows load as zeros, and the bias skips them)
-      uint32_t a = 0;
+      float a = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) a = max(a, abs_bits(v[j]));
-      const uint32_t ex = ckpt_exponent(a);
+      for (int j = 0; j < 32; j += 2) a = max_abs3(a, v[j], v[j + 1]);
+      const uint32_t ex = ckpt_exponent(abs_bits(a));
       const float inv = ckpt_inverse(ex);
       const uint32_t mask = ex == 255u ? 0u : 0xffffffffu;
       uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = ckpt_q4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv, mask);
+      for (int j = 0; j < 8; ++j) w[j] = ckpt_q4(make_float2(v[4 * j], v[4 * j + 1]), make_float2(v[4 * j + 2], v[4 * j + 3]), inv, mask);
       int8_t* q = e.k.q + (long long)row * e.k.ld_q + col;
       if (aligned32(q)) {
         st_global_v8(q, w);
@@ -165,10 +168,10 @@ __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int 
         if (j < n) {
           Vec8<T> x;
           x.load(r + j);
-          float f[8];
+          f2 f[4];
           x.get(f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[j + i] += f[i];
+          for (int i = 0; i < 4; ++i) v[j + 2 * i] += f[i].x, v[j + 2 * i + 1] += f[i].y;
         }
     }
     store16x32<T>(static_cast<T*>(e.out) + (long long)row * e.ld_out + col, v, n);
