@@ -96,10 +96,11 @@ mao_status run(const ActArgs& a, int act, dim3 grid, cudaStream_t s) {
 
 }  // namespace
 
-// About six blocks per SM of a B200, at least 32 rows each; chunks <= 888 fits grid.y.
+// About eight waves of the three blocks that an SM of a B200 holds, so that the last wave's
+// idle share is small, at least 32 rows each; chunks <= 3552 fits grid.y.
 int act_bwd_chunk(int rows, int cols) {
   const int strips = (cols + 255) / 256;
-  const int want = std::max(1, 888 / strips);
+  const int want = std::max(1, 3552 / strips);
   const int chunks = std::max(1, std::min(want, (rows + 31) / 32));
   return (rows + chunks - 1) / chunks;
 }

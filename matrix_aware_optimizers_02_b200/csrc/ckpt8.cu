@@ -12,35 +12,37 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 
-// A thread's walk over vectors of 8, `stride` = gridDim.x * kThreads apart: one division at its
-// start, then additions (dr rows and dv vectors per step; a division per vector made the read
-// back issue-bound: 133 instructions per vector).
+// A thread's walk over vectors of 8: a block takes tiles of kUnroll * kThreads consecutive
+// vectors, gridDim.x tiles apart, a thread kUnroll of each, kThreads apart.  One division at
+// the start, then additions: (row, vector) moves by (dr, dv) inside a tile and by (tr, tv) to
+// the next one (a division per vector made the read-back issue-bound: 133 instructions each).
+struct Steps {
+  long long total;  // vectors
+  int rows, vpr, dr, dv, tr, tv;
+};
 struct Walk {
   long long row;
   int v;
-  __device__ __forceinline__ Walk(int vpr) {
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;  // below 2^31
-    row = (uint32_t)i / (uint32_t)vpr;
-    v = (int)((uint32_t)i - (uint32_t)row * (uint32_t)vpr);
+  __device__ __forceinline__ Walk(const Steps& s) {
+    const uint32_t i = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;  // below 2^31
+    const uint32_t r = i / (uint32_t)s.vpr;
+    row = r;
+    v = (int)(i - r * (uint32_t)s.vpr);
   }
-  __device__ __forceinline__ void next(int dr, int dv, int vpr) {
+  __device__ __forceinline__ void move(int dr, int dv, int vpr) {
     row += dr;
     v += dv;
     if (v >= vpr) v -= vpr, ++row;
   }
 };
-struct Steps {
-  long long total;  // vectors
-  int rows, vpr, dr, dv;
-};
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x, long long ld_x, CkptView k, Steps st,
                                                          int cols) {
-  Walk at(st.vpr);
-  const long long stride = (long long)gridDim.x * kThreads;
+  Walk at(st);
+  const long long tile = kThreads * kUnroll;
   // uniform over the block: lanes behind the last vector take part in the shuffles
-  for (long long i = (long long)blockIdx.x * kThreads; i < st.total; i += kUnroll * stride) {
+  for (long long i = blockIdx.x * tile; i < st.total; i += gridDim.x * tile) {
     Vec8<T> v[kUnroll];
     long long row[kUnroll];
     int col[kUnroll];
@@ -50,8 +52,9 @@ __global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x
       col[u] = at.v * 8;
       if (at.row < st.rows && col[u] < cols) v[u].load(x + at.row * ld_x + col[u]);
       else v[u].zero();
-      at.next(st.dr, st.dv, st.vpr);
+      at.move(st.dr, st.dv, st.vpr);
     }
+    at.move(st.tr, st.tv, st.vpr);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const uint32_t amax = v[u].block_max();  // 4 | vpr: a block's lanes are all in or all out
@@ -64,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x
 
 template <class T, int ACT>
 __global__ void __launch_bounds__(kThreads) restore_kernel(CkptView k, T* __restrict__ y, long long ld_y, Steps st) {
-  Walk at(st.vpr);
+  Walk at(st);
   while (at.row < st.rows) {
     CkptVec8 v[kUnroll];
     long long row[kUnroll];
@@ -74,8 +77,9 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(CkptView k, T* __rest
       row[u] = at.row;
       col[u] = at.v * 8;
       if (at.row < st.rows) v[u].load(k, at.row, col[u]);
-      at.next(st.dr, st.dv, st.vpr);
+      at.move(st.dr, st.dv, st.vpr);
     }
+    at.move(st.tr, st.tv, st.vpr);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (row[u] >= st.rows) break;
@@ -99,10 +103,13 @@ unsigned steps_of(int rows, int vpr, int sms, Steps* s) {
   s->total = (long long)rows * vpr;
   s->rows = rows;
   s->vpr = vpr;
-  const long long want = (s->total + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  const long long grid = std::min<long long>(want, 8ll * sms);
-  s->dr = (int)(grid * kThreads / vpr);
-  s->dv = (int)(grid * kThreads % vpr);
+  const long long tile = kThreads * kUnroll;
+  const long long grid = std::min<long long>((s->total + tile - 1) / tile, 8ll * sms);
+  s->dr = kThreads / vpr;
+  s->dv = kThreads % vpr;
+  const long long rest = (grid - 1) * tile;  // a tile's kUnroll moves have covered the first
+  s->tr = (int)(rest / vpr);
+  s->tv = (int)(rest % vpr);
   return (unsigned)grid;
 }
 template <class T>

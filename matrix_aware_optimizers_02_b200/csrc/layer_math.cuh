@@ -139,9 +139,17 @@ struct Vec8<float> {
     a = *reinterpret_cast<const float4*>(p);
     b = *(reinterpret_cast<const float4*>(p) + 1);
   }
+  // a whole 32-byte sector per lane where the address allows (two 16-byte stores write each
+  // sector in halves: 82 against 61 us for 16384 x 4096 read back)
   __device__ __forceinline__ void store(float* p) const {
-    *reinterpret_cast<float4*>(p) = a;
-    *(reinterpret_cast<float4*>(p) + 1) = b;
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a.x), "f"(a.y), "f"(a.z),
+                   "f"(a.w), "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
+                   : "memory");
+    } else {
+      *reinterpret_cast<float4*>(p) = a;
+      *(reinterpret_cast<float4*>(p) + 1) = b;
+    }
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(f2 (&v)[4]) const {
