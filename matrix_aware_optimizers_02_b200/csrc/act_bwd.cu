@@ -2,8 +2,9 @@
 // the column sums of the unrounded dz for the bias gradient in the same pass.
 //
 // HBM-bound: dy 2 + z 2 (or 1 + 1/32 from a checkpoint) + dz 2 bytes per element.  A lane
-// owns 8 columns, a block 256 columns of a chunk of rows; each chunk leaves one partial row
-// of column sums, joined in order by a second kernel (no atomics: the same bits every run).
+// owns 16 columns, a block 512 columns of a chunk of rows, each warp every eighth row; a
+// thread reads its next three rows ahead by cp.async.  Each chunk leaves one partial row of
+// column sums, joined in order by a second kernel (no atomics: the same bits every run).
 #include "act_bwd.h"
 
 namespace mao {
@@ -19,88 +20,147 @@ struct ActArgs {
   int rows, cols, chunk;
 };
 
-constexpr int kRowsInFlight = 4;
+constexpr int kCols = 16;    // columns per lane
+constexpr int kStages = 4;   // rows read ahead per thread, less one
+constexpr int kThreads = 256;
+constexpr int kStrip = 32 * kCols;  // columns per block
+
+template <int ACT, bool KEPT>
+constexpr int kSlot = 32 + (ACT == MAO_ACT_NONE ? 0 : (KEPT ? 16 : 32));  // ring bytes per thread and row
 
 template <class T, int ACT, bool KEPT>
-__global__ void __launch_bounds__(256) act_bwd_kernel(const ActArgs a) {
-  __shared__ float2 sh[8][128];
+__global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const ActArgs a) {
+  constexpr bool HAS = ACT != MAO_ACT_NONE;
+  constexpr uint32_t kPiece = kThreads * 16;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const uint32_t slot = smem_u32(ring) + threadIdx.x * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = (blockIdx.x * 32 + lane) * 8;
+  // two vectors of 8 columns, 256 columns apart: neighbouring lanes read neighbouring 16 bytes
+  const int c = blockIdx.x * kStrip + lane * 8;
+  const int halves = c >= a.cols ? 0 : (c + 256 < a.cols ? 2 : 1);  // vectors inside the row
   const long long r_end = min((long long)a.rows, ((long long)blockIdx.y + 1) * a.chunk);
-  f2 sum[4];
+  const long long r_begin = (long long)blockIdx.y * a.chunk + warp;
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* z = static_cast<const T*>(a.z);
+  auto fetch = [&](long long r, int stage) {
+    const uint32_t dst = slot + stage * (kSlot<ACT, KEPT> * kThreads);
+    const bool in = r < r_end;
+    const T* p = dy + (in ? r : 0) * a.ld_dy + c;
+    cp_async16(dst, in && halves > 0 ? p : dy, in && halves > 0);
+    cp_async16(dst + kPiece, in && halves > 1 ? p + 256 : dy, in && halves > 1);
+    if constexpr (HAS && KEPT) {
+      const int8_t* q = a.k.q + (in ? r : 0) * a.k.ld_q + c;
+      const uint32_t dk = dst + 2 * kPiece - threadIdx.x * 8;  // 8 bytes per thread and vector
+      cp_async8(dk, in && halves > 0 ? q : a.k.q, in && halves > 0);
+      cp_async8(dk + kPiece / 2, in && halves > 1 ? q + 256 : a.k.q, in && halves > 1);
+    } else if constexpr (HAS) {
+      const T* q = z + (in ? r : 0) * a.ld_z + c;
+      cp_async16(dst + 2 * kPiece, in && halves > 0 ? q : z, in && halves > 0);
+      cp_async16(dst + 3 * kPiece, in && halves > 1 ? q + 256 : z, in && halves > 1);
+    }
+    cp_async_commit();
+  };
+  struct Bytes {  // of the two vectors' checkpoint blocks
+    uint32_t e[2];
+  };
+  auto fetch_e = [&](long long r) {
+    Bytes b = {{1u, 1u}};
+    if constexpr (HAS && KEPT) {
+      const uint8_t* e = a.k.e + r * a.k.ld_e + (c >> 5);
+      if (r < r_end && halves > 0) b.e[0] = e[0];
+      if (r < r_end && halves > 1) b.e[1] = e[8];
+    }
+    return b;
+  };
 #pragma unroll
-  for (int j = 0; j < 4; ++j) sum[j] = dup2(0.0f);
-  if (c < a.cols) {
-    for (long long r0 = (long long)blockIdx.y * a.chunk + warp; r0 < r_end; r0 += 8 * kRowsInFlight) {
-      Vec8<T> g[kRowsInFlight];
-      Vec8<T> z[kRowsInFlight];
-      CkptVec8 zk[kRowsInFlight];
+  for (int d = 0; d < kStages - 1; ++d) fetch(r_begin + 8 * d, d);
+  Bytes e0 = fetch_e(r_begin), e1 = fetch_e(r_begin + 8), e2 = fetch_e(r_begin + 16);
+  f2 sum[8];
 #pragma unroll
-      for (int i = 0; i < kRowsInFlight; ++i) {
-        const long long r = r0 + 8 * i;
-        if (r < r_end) {
-          g[i].load(static_cast<const T*>(a.dy) + r * a.ld_dy + c);
-          if constexpr (ACT != MAO_ACT_NONE) {
-            if constexpr (KEPT) zk[i].load(a.k, r, c);
-            else z[i].load(static_cast<const T*>(a.z) + r * a.ld_z + c);
-          }
+  for (int j = 0; j < 8; ++j) sum[j] = dup2(0.0f);
+  int stage = 0;
+  for (long long r = r_begin; r < r_end; r += 8) {
+    fetch(r + 8 * (kStages - 1), stage == 0 ? kStages - 1 : stage - 1);
+    const Bytes e = e0;
+    e0 = e1, e1 = e2, e2 = fetch_e(r + 24);
+    cp_async_wait<kStages - 1>();
+    const uint32_t src = slot + stage * (kSlot<ACT, KEPT> * kThreads);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Vec8<T> g;
+      g.w = lds16(src + h * kPiece);
+      f2 d[4];
+      g.get(d);
+      if constexpr (HAS) {
+        f2 f[4];
+        if constexpr (KEPT) {
+          CkptVec8 k;
+          k.w = lds8(src + 2 * kPiece - threadIdx.x * 8 + h * (kPiece / 2));
+          k.e = e.e[h];
+          k.get(f);
+        } else {
+          Vec8<T> v;
+          v.w = lds16(src + (2 + h) * kPiece);
+          v.get(f);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], act_slope<ACT>(f[j]));
+        Vec8<T> o;
+        o.set(d);
+        if (a.dz != nullptr && h < halves) o.store(static_cast<T*>(a.dz) + r * a.ld_dz + c + 256 * h);
       }
 #pragma unroll
-      for (int i = 0; i < kRowsInFlight; ++i) {
-        const long long r = r0 + 8 * i;
-        if (r < r_end) {
-          f2 d[4];
-          g[i].get(d);
-          if constexpr (ACT != MAO_ACT_NONE) {
-            f2 f[4];
-            if constexpr (KEPT) zk[i].get(f);
-            else z[i].get(f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], act_slope<ACT>(f[j]));
-            Vec8<T> o;
-            o.set(d);
-            if (a.dz != nullptr) o.store(static_cast<T*>(a.dz) + r * a.ld_dz + c);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], d[j]);
-        }
-      }
+      for (int j = 0; j < 4; ++j) sum[4 * h + j] = add2(sum[4 * h + j], d[j]);
     }
   }
+  cp_async_wait<0>();
   if (a.part == nullptr) return;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) sh[warp][lane * 4 + j] = sum[j];
+  // the warps' sums joined in warp order, through the ring's memory
   __syncthreads();
-  const float* p = reinterpret_cast<const float*>(sh);
-  float s = 0.0f;
+  float* sh = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int w = 0; w < 8; ++w) s += p[w * 256 + threadIdx.x];
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col < a.cols) a.part[(long long)blockIdx.y * a.cols + col] = s;
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<f2*>(sh + warp * kStrip + (j >> 2) * 256 + lane * 8 + 2 * (j & 3)) = sum[j];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kStrip / kThreads; ++i) {
+    const int k = i * kThreads + threadIdx.x;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sh[w * kStrip + k];
+    if (blockIdx.x * kStrip + k < a.cols) a.part[(long long)blockIdx.y * a.cols + blockIdx.x * kStrip + k] = s;
+  }
+}
+
+template <class T, int ACT, bool KEPT>
+mao_status run_one(const ActArgs& a, dim3 grid, cudaStream_t s) {
+  constexpr int smem = kStages * kSlot<ACT, KEPT> * kThreads;  // at least the 16 KB of the joined sums
+  static_assert(smem >= 8 * kStrip * (int)sizeof(float), "the joined sums use the ring's memory");
+  static std::atomic<bool> done[64];
+  MAO_TRY(allow_smem(act_bwd_kernel<T, ACT, KEPT>, smem, done));
+  act_bwd_kernel<T, ACT, KEPT><<<grid, kThreads, smem, s>>>(a);
+  return launched();
 }
 
 template <class T, bool KEPT>
 mao_status run(const ActArgs& a, int act, dim3 grid, cudaStream_t s) {
   switch (act) {
-    case MAO_ACT_NONE: act_bwd_kernel<T, MAO_ACT_NONE, false><<<grid, 256, 0, s>>>(a); break;
-    case MAO_ACT_RELU: act_bwd_kernel<T, MAO_ACT_RELU, KEPT><<<grid, 256, 0, s>>>(a); break;
-    case MAO_ACT_RELU2: act_bwd_kernel<T, MAO_ACT_RELU2, KEPT><<<grid, 256, 0, s>>>(a); break;
-    case MAO_ACT_GELU: act_bwd_kernel<T, MAO_ACT_GELU, KEPT><<<grid, 256, 0, s>>>(a); break;
-    case MAO_ACT_GELU_TANH: act_bwd_kernel<T, MAO_ACT_GELU_TANH, KEPT><<<grid, 256, 0, s>>>(a); break;
-    case MAO_ACT_SILU: act_bwd_kernel<T, MAO_ACT_SILU, KEPT><<<grid, 256, 0, s>>>(a); break;
+    case MAO_ACT_NONE: return run_one<T, MAO_ACT_NONE, false>(a, grid, s);
+    case MAO_ACT_RELU: return run_one<T, MAO_ACT_RELU, KEPT>(a, grid, s);
+    case MAO_ACT_RELU2: return run_one<T, MAO_ACT_RELU2, KEPT>(a, grid, s);
+    case MAO_ACT_GELU: return run_one<T, MAO_ACT_GELU, KEPT>(a, grid, s);
+    case MAO_ACT_GELU_TANH: return run_one<T, MAO_ACT_GELU_TANH, KEPT>(a, grid, s);
+    case MAO_ACT_SILU: return run_one<T, MAO_ACT_SILU, KEPT>(a, grid, s);
     default: return MAO_ERR_INVALID_ARG;
   }
-  return launched();
 }
 
 }  // namespace
 
-// About eight waves of the three blocks that an SM of a B200 holds, so that the last wave's
-// idle share is small, at least 32 rows each; chunks <= 3552 fits grid.y.
+// Two full waves of the three blocks that an SM of a B200 holds, at least 32 rows each.
 int act_bwd_chunk(int rows, int cols) {
-  const int strips = (cols + 255) / 256;
-  const int want = std::max(1, 3552 / strips);
+  const int strips = (cols + kStrip - 1) / kStrip;
+  const int want = std::max(1, 888 / strips);
   const int chunks = std::max(1, std::min(want, (rows + 31) / 32));
   return (rows + chunks - 1) / chunks;
 }
@@ -113,7 +173,7 @@ mao_status act_bwd_launch(const void* dy, long long ld_dy, const void* z, long l
   a.ld_dy = ld_dy, a.ld_z = ld_z, a.ld_dz = ld_dz;
   a.rows = rows, a.cols = cols;
   a.chunk = act_bwd_chunk(rows, cols);
-  const dim3 grid((cols + 255) / 256, (rows + a.chunk - 1) / a.chunk);
+  const dim3 grid((cols + kStrip - 1) / kStrip, (rows + a.chunk - 1) / a.chunk);
   const double z_bytes = act == MAO_ACT_NONE ? 0.0 : (kept ? 1.0 + 1.0 / 32 : 2.0);
   LaunchScope ls(stream, MAO_K_ACT_BWD, 0.0, (double)rows * cols * (2.0 + z_bytes + (dz ? 2.0 : 0.0)));
   if (dtype == MAO_BF16)

@@ -2,6 +2,7 @@
 // operators that one entry point calls of another.
 #pragma once
 
+#include <atomic>
 #include <climits>
 
 #include "host_common.h"
@@ -31,6 +32,18 @@ inline mao_status check_ckpt(const mao_ckpt8& c, int rows, int cols) {
 inline CkptView view(const mao_ckpt8& c) { return CkptView{c.q, c.e, c.ld_q, c.ld_e}; }
 
 inline mao_status launched() { return cudaGetLastError() == cudaSuccess ? MAO_OK : MAO_ERR_CUDA; }
+
+// A kernel's dynamic shared memory limit, raised once per device.
+template <class K>
+mao_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
+  int d = 0;
+  MAO_CUDA_TRY(cudaGetDevice(&d));  // device_info has bounded it
+  if (!done[d].load(std::memory_order_acquire)) {
+    MAO_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done[d].store(true, std::memory_order_release);
+  }
+  return MAO_OK;
+}
 
 // y = act(value of c); arguments checked by the caller, rows >= 1
 mao_status restore_launch(const CkptView& c, int rows, int cols, int act, void* y, int dtype, long long ld_y,

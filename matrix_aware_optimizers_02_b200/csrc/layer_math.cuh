@@ -238,12 +238,12 @@ struct Slot8 {
 // Two values at a time.  sigmoid(z) = 1 / (1 + exp(-z)); exp(-z) = inf gives 0, as it should.
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float rcp_fast(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 constexpr float kLog2e = 1.4426950408889634f;

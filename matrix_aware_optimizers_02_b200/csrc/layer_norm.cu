@@ -11,8 +11,6 @@
 //
 // Mean and variance: two passes over the registers (sum of x, then of (x - mean)^2), so
 // a large mean costs no digits.
-#include <atomic>
-
 #include "layer_host.h"
 
 namespace mao {
@@ -447,18 +445,6 @@ int bwd_blocks(int rows, int cols, int sms) {
   MAO_NORM_SIZES(MAO_CASE)
 #undef MAO_CASE
   return n;
-}
-
-// A kernel's dynamic shared memory limit, raised once per device.
-template <class K>
-mao_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
-  int d = 0;
-  MAO_CUDA_TRY(cudaGetDevice(&d));  // device_info has bounded it
-  if (!done[d].load(std::memory_order_acquire)) {
-    MAO_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-    done[d].store(true, std::memory_order_release);
-  }
-  return MAO_OK;
 }
 
 template <class T, int G, int VPT>

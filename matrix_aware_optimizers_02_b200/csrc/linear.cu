@@ -1,7 +1,5 @@
 // The linear layer and its gradient (mao_linear, mao_linear_backward): argument checks,
 // the choice of tiles and K slices, and the launches.
-#include <atomic>
-
 #include "act_bwd.h"
 #include "linear_gemm.cuh"
 
@@ -51,13 +49,8 @@ template <class T, int KIND, int A_MN, int B_MN, bool PAIR>
 mao_status launch_product(const LinParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   using Cfg = LinCfg<PAIR>;
   auto kern = PAIR ? lin_pair_kernel<T, KIND, A_MN, B_MN> : lin_kernel<T, KIND, A_MN, B_MN>;
-  int d = 0;
-  MAO_CUDA_TRY(cudaGetDevice(&d));
-  static std::atomic<bool> attr_set[64];  // device_info bounds the device number
-  if (!attr_set[d].load(std::memory_order_acquire)) {
-    MAO_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES));
-    attr_set[d].store(true, std::memory_order_release);
-  }
+  static std::atomic<bool> done[64];
+  MAO_TRY(allow_smem(kern, Cfg::SMEM_BYTES, done));
   const int workers = std::min(p.items, PAIR ? dev.sm_count / 2 : dev.sm_count);
   kern<<<PAIR ? 2 * workers : workers, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(p);
   return launched();
