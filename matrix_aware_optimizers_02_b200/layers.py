@@ -19,7 +19,6 @@ calls.  Argument marshalling only; every arithmetic step runs in the library's k
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple, Union
 
@@ -82,13 +81,14 @@ def _act(name: str) -> int:
     return L.ACTIVATIONS[name]
 
 
-def _on(device):
-    """The device's context, entered only where it is not the current one."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _elsewhere(device) -> bool:
+    """Whether the tensors' device is not the current one; such a call is made again with it current."""
+    return device.index != torch.cuda.current_device()
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+# torch.cuda.current_stream(device).cuda_stream without building a Stream object: 0.1 against
+# 2.2 us, of a call that takes about 10
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -125,8 +125,11 @@ class Checkpoint8:
     @classmethod
     def empty(cls, rows: int, cols: int, dtype: torch.dtype, device) -> "Checkpoint8":
         blocks = (cols + 31) // 32
-        return cls(torch.empty((rows, 32 * blocks), dtype=torch.int8, device=device),
-                   torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols, dtype)
+        k = object.__new__(cls)  # nothing to check
+        k.q = torch.empty((rows, 32 * blocks), dtype=torch.int8, device=device)
+        k.e = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
+        k.cols, k.dtype = cols, dtype
+        return k
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -150,12 +153,14 @@ class Checkpoint8:
         if dtype not in _DTYPES:
             raise TypeError(f"dtype {dtype} not supported")
         dev = self.q.device
-        with _on(dev):
-            y = torch.empty(self.shape, dtype=dtype, device=dev)
-            c = self._c()
-            L.check(L.load().mao_checkpoint8_restore(ctypes.byref(c), self.q.shape[0], self.cols, a, y.data_ptr(),
-                                                     _DTYPES[dtype], self.cols, _stream(dev)),
-                    "mao_checkpoint8_restore")
+        if _elsewhere(dev):
+            with torch.cuda.device(dev):
+                return self.restore(act, dtype)
+        rows = self.q.shape[0]
+        y = self.q.new_empty((rows, self.cols), dtype=dtype)
+        c = self._c()
+        L.check(L.load().mao_checkpoint8_restore(ctypes.byref(c), rows, self.cols, a, y.data_ptr(), _DTYPES[dtype],
+                                                 self.cols, _stream(dev.index)), "mao_checkpoint8_restore")
         return y
 
 
@@ -164,11 +169,14 @@ def checkpoint8(x: torch.Tensor) -> Checkpoint8:
     ld = _check_acts("x", x)
     if x.dtype not in _DTYPES:
         raise TypeError(f"x dtype {x.dtype} not supported (float32, bfloat16 or float16)")
-    with _on(x.device):
-        k = Checkpoint8.empty(x.shape[0], x.shape[1], x.dtype, x.device)
-        c = k._c()
-        L.check(L.load().mao_checkpoint8(x.data_ptr(), _DTYPES[x.dtype], x.shape[0], x.shape[1], ld, ctypes.byref(c),
-                                         _stream(x.device)), "mao_checkpoint8")
+    dev = x.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return checkpoint8(x)
+    k = Checkpoint8.empty(x.shape[0], x.shape[1], x.dtype, dev)
+    c = k._c()
+    L.check(L.load().mao_checkpoint8(x.data_ptr(), _DTYPES[x.dtype], x.shape[0], x.shape[1], ld, ctypes.byref(c),
+                                     _stream(dev.index)), "mao_checkpoint8")
     return k
 
 
@@ -188,15 +196,16 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     _check_param("weight", weight, cols, dev, (torch.float32, x.dtype))
     if bias is not None:
         _check_param("bias", bias, cols, dev, (weight.dtype,))
-    with _on(dev):
-        y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-        stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
-        mean, rstd = stats[0], stats[1]
-        kept = Checkpoint8.empty(rows, cols, x.dtype, dev) if checkpoint else None
-        a = L.LayerNormArgs(rows, cols, _DTYPES[x.dtype], _DTYPES[weight.dtype], x.data_ptr(), ld, weight.data_ptr(),
-                            _ptr(bias), eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
-                            kept._c() if checkpoint else _NO_CKPT)
-        L.check(L.load().mao_layer_norm(ctypes.byref(a), _stream(dev)), "mao_layer_norm")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return layer_norm(x, weight, bias, eps=eps, checkpoint=checkpoint)
+    y = x.new_empty((rows, cols))
+    mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
+    kept = Checkpoint8.empty(rows, cols, x.dtype, dev) if checkpoint else None
+    a = L.LayerNormArgs(rows, cols, _DTYPES[x.dtype], _DTYPES[weight.dtype], x.data_ptr(), ld, weight.data_ptr(),
+                        _ptr(bias), eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
+                        kept._c() if checkpoint else _NO_CKPT)
+    L.check(L.load().mao_layer_norm(ctypes.byref(a), _stream(dev.index)), "mao_layer_norm")
     return y, mean, rstd, kept
 
 
@@ -230,19 +239,20 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8], w
     _check_param("rstd", rstd, rows, dev, (torch.float32,))
     ld_dres = _check_acts("dres", dres, (rows, cols), dev, dy.dtype) if dres is not None else 0
     lib = L.load()
-    with _on(dev):
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
-        dwb = torch.empty((2, cols), dtype=torch.float32, device=dev)
-        dw, db = dwb[0], dwb[1]
-        a = L.LayerNormBackwardArgs(rows, cols, _DTYPES[dy.dtype], _DTYPES[weight.dtype], dy.data_ptr(), ld_dy, xp,
-                                    ld_x, xc, weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dres),
-                                    ld_dres, dx.data_ptr(), cols, dw.data_ptr(), db.data_ptr())
-        n = ctypes.c_size_t(0)
-        L.check(lib.mao_layer_norm_backward_workspace_size(ctypes.byref(a), ctypes.byref(n)),
-                "mao_layer_norm_backward_workspace_size")
-        ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        L.check(lib.mao_layer_norm_backward(ctypes.byref(a), ws.data_ptr(), n.value, _stream(dev)),
-                "mao_layer_norm_backward")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return layer_norm_backward(dy, x, weight, mean, rstd, dres=dres)
+    dx = dy.new_empty((rows, cols))
+    dw, db = dy.new_empty(cols, dtype=torch.float32), dy.new_empty(cols, dtype=torch.float32)
+    a = L.LayerNormBackwardArgs(rows, cols, _DTYPES[dy.dtype], _DTYPES[weight.dtype], dy.data_ptr(), ld_dy, xp,
+                                ld_x, xc, weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dres),
+                                ld_dres, dx.data_ptr(), cols, dw.data_ptr(), db.data_ptr())
+    n = ctypes.c_size_t(0)
+    L.check(lib.mao_layer_norm_backward_workspace_size(ctypes.byref(a), ctypes.byref(n)),
+            "mao_layer_norm_backward_workspace_size")
+    ws = dy.new_empty(n.value, dtype=torch.uint8)
+    L.check(lib.mao_layer_norm_backward(ctypes.byref(a), ws.data_ptr(), n.value, _stream(dev.index)),
+            "mao_layer_norm_backward")
     return dx, dw, db
 
 
@@ -279,22 +289,24 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
         _check_param("bias", bias, m, dev, (torch.float32, dt))
     ld_res = _check_acts("residual", residual, (rows, m), dev, dt) if residual is not None else 0
     lib = L.load()
-    with _on(dev):
-        y = torch.empty((rows, m), dtype=dt, device=dev)
-        kept, z, zc = None, None, _NO_CKPT
-        if checkpoint == "tensor":
-            kept = z = torch.empty((rows, m), dtype=dt, device=dev)
-        elif checkpoint:
-            kept = Checkpoint8.empty(rows, m, dt, dev)
-            zc = kept._c()
-        a = L.LinearArgs(rows, n, m, _DTYPES[dt], x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias),
-                         _DTYPES[bias.dtype] if bias is not None else 0, a_id, _ptr(residual), ld_res, y.data_ptr(),
-                         m, _ptr(z), m, zc)
-        nb = ctypes.c_size_t(0)
-        ref = ctypes.byref(a)
-        L.check(lib.mao_linear_workspace_size(ref, ctypes.byref(nb)), "mao_linear_workspace_size")
-        ws = torch.empty(nb.value, dtype=torch.uint8, device=dev) if nb.value else None
-        L.check(lib.mao_linear(ref, _ptr(ws), nb.value, _stream(dev)), "mao_linear")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return linear(x, W, bias, act=act, residual=residual, checkpoint=checkpoint)
+    y = x.new_empty((rows, m))
+    kept, z, zc = None, None, _NO_CKPT
+    if checkpoint == "tensor":
+        kept = z = x.new_empty((rows, m))
+    elif checkpoint:
+        kept = Checkpoint8.empty(rows, m, dt, dev)
+        zc = kept._c()
+    a = L.LinearArgs(rows, n, m, _DTYPES[dt], x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias),
+                     _DTYPES[bias.dtype] if bias is not None else 0, a_id, _ptr(residual), ld_res, y.data_ptr(),
+                     m, _ptr(z), m, zc)
+    nb = ctypes.c_size_t(0)
+    ref = ctypes.byref(a)
+    L.check(lib.mao_linear_workspace_size(ref, ctypes.byref(nb)), "mao_linear_workspace_size")
+    ws = x.new_empty(nb.value, dtype=torch.uint8) if nb.value else None
+    L.check(lib.mao_linear(ref, _ptr(ws), nb.value, _stream(dev.index)), "mao_linear")
     return y, kept
 
 
@@ -339,26 +351,30 @@ def linear_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8], W: to
     if accumulate and dw_dtype != torch.float32:
         raise TypeError("accumulate needs a float32 dw")
     lib = L.load()
-    with _on(dev):
-        dx = torch.empty((rows, n), dtype=dt, device=dev) if need_dx else None
-        if dw is None and need_dw:
-            dw = torch.empty((m, n), dtype=dw_dtype, device=dev)
-        db = torch.empty(m, dtype=torch.float32, device=dev) if need_db else None
-        a = L.LinearBackwardArgs(rows, n, m, _DTYPES[dt], dy.data_ptr(), ld_dy, xp, ld_x, xc, W.data_ptr(), a_id, zp,
-                                 ld_z, zc, _ptr(dx), n, _ptr(dw), _DTYPES[dw_dtype], int(bool(accumulate)), _ptr(db))
-        nb = ctypes.c_size_t(0)
-        ref = ctypes.byref(a)
-        L.check(lib.mao_linear_backward_workspace_size(ref, ctypes.byref(nb)), "mao_linear_backward_workspace_size")
-        ws = torch.empty(nb.value, dtype=torch.uint8, device=dev) if nb.value else None
-        L.check(lib.mao_linear_backward(ref, _ptr(ws), nb.value, _stream(dev)), "mao_linear_backward")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return linear_backward(dy, x, W, z=z, act=act, dw=dw, accumulate=accumulate, dw_dtype=dw_dtype,
+                                   need_dx=need_dx, need_dw=need_dw, need_db=need_db)
+    dx = dy.new_empty((rows, n)) if need_dx else None
+    if dw is None and need_dw:
+        dw = dy.new_empty((m, n), dtype=dw_dtype)
+    db = dy.new_empty(m, dtype=torch.float32) if need_db else None
+    a = L.LinearBackwardArgs(rows, n, m, _DTYPES[dt], dy.data_ptr(), ld_dy, xp, ld_x, xc, W.data_ptr(), a_id, zp,
+                             ld_z, zc, _ptr(dx), n, _ptr(dw), _DTYPES[dw_dtype], int(bool(accumulate)), _ptr(db))
+    nb = ctypes.c_size_t(0)
+    ref = ctypes.byref(a)
+    L.check(lib.mao_linear_backward_workspace_size(ref, ctypes.byref(nb)), "mao_linear_backward_workspace_size")
+    ws = dy.new_empty(nb.value, dtype=torch.uint8) if nb.value else None
+    L.check(lib.mao_linear_backward(ref, _ptr(ws), nb.value, _stream(dev.index)), "mao_linear_backward")
     return dx, dw, db
 
 
 def layer_status(device=None) -> Tuple[int, int]:
     """(status, site) of the first condition that these operators recorded on the device
     since the last call (0: none).  Synchronises the device's current stream."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    dev = torch.device("cuda" if device is None else device)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
     where = ctypes.c_int32(0)
-    with torch.cuda.device(dev):
-        st = L.load().mao_layer_status(_stream(dev), ctypes.byref(where))
+    with torch.cuda.device(index):
+        st = L.load().mao_layer_status(_stream(index), ctypes.byref(where))
     return st, where.value
