@@ -7,37 +7,46 @@ namespace mao {
 namespace {
 
 // ------------------------------------------------------------------ plan
+enum LinTile : int { TILE_PAIR256 = 0, TILE_PAIR128 = 1, TILE_ONE = 2 };
+constexpr int kTileM[3] = {256, 256, 128}, kTileN[3] = {256, 128, 128};
+
 struct LinPlan {
-  bool pair = false;
-  int tiles_m = 0, tiles_n = 0, nk = 0, slices = 1, slice_blocks = 0;
+  int tile = TILE_ONE;
+  int tiles_m = 0, tiles_n = 0, nk = 0, full = 0, slices = 1, slice_blocks = 0;
+  int items = 0;
   size_t part_bytes = 0;
 };
 
 // Tiles and K slices of an M x N x K product, from its sizes alone (and so the same on
-// every device and in the workspace query).  Estimated clocks of a wave of work items.
+// every device and in the workspace query): the cheapest by estimated clocks.
 constexpr int kPlanSms = 148;
 
 bool plan_of(long long M, long long N, long long K, LinPlan* out) {
+  // clocks of a k-block of 64, of the last epilogue, and of a join of the slices
+  constexpr double kBlock[3] = {530.0, 400.0, 700.0}, kTail[3] = {5000.0, 4000.0, 4000.0};
+  constexpr double kJoin = 7000.0, kJoinBytes = 2000.0;  // launch; bytes per clock
   const long long nk = (K + 63) / 64;
   double best = 1e300;
-  for (int pair = 0; pair < 2; ++pair) {
-    const long long edge = pair ? 256 : 128;
-    const long long tm = (M + edge - 1) / edge, tn = (N + edge - 1) / edge, tiles = tm * tn;
-    if (tiles > (1ll << 28)) continue;
-    const long long workers = pair ? kPlanSms / 2 : kPlanSms;
-    const double block = pair ? 530.0 : 330.0, tail = pair ? 6000.0 : 4000.0;
+  for (int t = 0; t < 3; ++t) {
+    const long long tm = (M + kTileM[t] - 1) / kTileM[t], tn = (N + kTileN[t] - 1) / kTileN[t], tiles = tm * tn;
+    if (tiles > (1ll << 27)) continue;
+    const long long workers = t == TILE_ONE ? kPlanSms : kPlanSms / 2;
+    const long long waves = tiles / workers, rest = tiles - waves * workers;
     for (int s = 1; s <= 16; ++s) {
       const long long sb = (nk + s - 1) / s;
-      if (s > 1 && (sb < 4 || (nk + sb - 1) / sb != s)) continue;
-      const double waves = (double)((tiles * s + workers - 1) / workers);
-      double cost = waves * sb * block + tail;
-      if (s > 1) cost += 6000.0 + (double)M * (double)N * 8.0 * s / 2800.0;
+      if (s > 1 && (rest == 0 || sb < 4 || (nk + sb - 1) / sb != s)) break;
+      const long long rounds = (rest * s + workers - 1) / workers;
+      double cost = (double)(waves * nk + rounds * sb) * kBlock[t] + kTail[t];
+      const double bytes = s > 1 ? 4.0 * s * (double)rest * kTileM[t] * kTileN[t] : 0.0;
+      if (s > 1) cost += kJoin + 2.0 * bytes / kJoinBytes;
       if (cost < best) {
         best = cost;
-        out->pair = pair != 0;
+        out->tile = t;
         out->tiles_m = (int)tm, out->tiles_n = (int)tn, out->nk = (int)nk;
+        out->full = (int)(s > 1 ? tiles - rest : tiles);
         out->slices = s, out->slice_blocks = (int)sb;
-        out->part_bytes = s > 1 ? sizeof(float) * (size_t)s * (size_t)M * (size_t)N : 0;
+        out->items = out->full + (int)(tiles - out->full) * s;
+        out->part_bytes = (size_t)bytes;
       }
     }
   }
@@ -45,10 +54,12 @@ bool plan_of(long long M, long long N, long long K, LinPlan* out) {
 }
 
 // ------------------------------------------------------------------ launch
-template <class T, int KIND, int A_MN, int B_MN, bool PAIR>
+template <class T, int KIND, int A_MN, int B_MN, bool PAIR, int BN>
 mao_status launch_product(const LinParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  using Cfg = LinCfg<PAIR>;
-  auto kern = PAIR ? lin_pair_kernel<T, KIND, A_MN, B_MN> : lin_kernel<T, KIND, A_MN, B_MN>;
+  using Cfg = LinCfg<PAIR, BN>;
+  void (*kern)(LinParams);
+  if constexpr (PAIR) kern = lin_pair_kernel<T, KIND, A_MN, B_MN, BN>;
+  else kern = lin_kernel<T, KIND, A_MN, B_MN>;
   static std::atomic<bool> done[64];
   MAO_TRY(allow_smem(kern, Cfg::SMEM_BYTES, done));
   const int workers = std::min(p.items, PAIR ? dev.sm_count / 2 : dev.sm_count);
@@ -61,9 +72,11 @@ struct Operand {
   long long inner, rows, ld;  // stored matrix: rows x inner
 };
 
-mao_status encode(CUtensorMap* map, int dtype, const Operand& o, bool mn) {
+// box_rows: the rows of a K-major tile that one CTA loads
+mao_status encode(CUtensorMap* map, int dtype, const Operand& o, bool mn, int box_rows) {
   return encode_3d(map, dtype == MAO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, o.p,
-                   (uint64_t)o.inner, (uint64_t)o.rows, 1, (uint64_t)o.ld, (uint64_t)o.ld * o.rows, 64, mn ? 64 : 128);
+                   (uint64_t)o.inner, (uint64_t)o.rows, 1, (uint64_t)o.ld, (uint64_t)o.ld * o.rows, 64,
+                   mn ? 64 : box_rows);
 }
 
 template <class T, int KIND, int A_MN, int B_MN>
@@ -72,24 +85,32 @@ mao_status product(const Operand& A, const Operand& B, const LinEpilogue& e, con
   DeviceInfo* dev = nullptr;
   MAO_TRY(device_info(&dev));
   LinParams p;
-  MAO_TRY(encode(&p.mapA, Elem<T>::kDtype, A, A_MN));
-  MAO_TRY(encode(&p.mapB, Elem<T>::kDtype, B, B_MN));
+  MAO_TRY(encode(&p.mapA, Elem<T>::kDtype, A, A_MN, 128));
+  MAO_TRY(encode(&p.mapB, Elem<T>::kDtype, B, B_MN, plan.tile == TILE_PAIR128 ? 64 : 128));
   p.e = e;
   p.part = part;
   p.tiles_m = plan.tiles_m, p.tiles_n = plan.tiles_n;
-  p.slices = plan.slices, p.slice_blocks = plan.slice_blocks, p.nk = plan.nk;
-  p.items = plan.tiles_m * plan.tiles_n * plan.slices;
+  p.full = plan.full, p.slices = plan.slices, p.slice_blocks = plan.slice_blocks;
+  p.nk = plan.nk, p.items = plan.items;
   const long long K = A_MN ? A.rows : A.inner;
   {
     LaunchScope ls(stream, kernel_id, 2.0 * e.M * (double)e.N * (double)K, bytes);
-    MAO_TRY(plan.pair ? (launch_product<T, KIND, A_MN, B_MN, true>(p, *dev, stream))
-                      : (launch_product<T, KIND, A_MN, B_MN, false>(p, *dev, stream)));
+    switch (plan.tile) {
+      case TILE_PAIR256: MAO_TRY((launch_product<T, KIND, A_MN, B_MN, true, 256>(p, *dev, stream))); break;
+      case TILE_PAIR128: MAO_TRY((launch_product<T, KIND, A_MN, B_MN, true, 128>(p, *dev, stream))); break;
+      default: MAO_TRY((launch_product<T, KIND, A_MN, B_MN, false, 128>(p, *dev, stream))); break;
+    }
   }
   if (plan.slices == 1) return MAO_OK;
-  const int cbs = (e.N + 31) / 32;
-  const long long total = (long long)e.M * cbs;
-  LaunchScope ls(stream, MAO_K_SLICE_REDUCE, 0.0, 4.0 * plan.slices * (double)e.M * e.N);
-  lin_reduce_kernel<T, KIND><<<(unsigned)((total + 127) / 128), 128, 0, stream>>>(e, part, plan.slices, cbs, total);
+  const LinJoin j{e, part, plan.tiles_m, plan.tiles_n, plan.full, plan.slices};
+  // at most one wave of tiles: far below 2^31 pieces
+  const int pieces = (plan.tiles_m * plan.tiles_n - plan.full) * (kTileM[plan.tile] * kTileN[plan.tile] / 32);
+  LaunchScope ls(stream, MAO_K_SLICE_REDUCE, 0.0, (double)plan.part_bytes);
+  switch (plan.tile) {
+    case TILE_PAIR256: lin_join_kernel<T, KIND, 256, 256><<<pieces / 128, 128, 0, stream>>>(j); break;
+    case TILE_PAIR128: lin_join_kernel<T, KIND, 256, 128><<<pieces / 128, 128, 0, stream>>>(j); break;
+    default: lin_join_kernel<T, KIND, 128, 128><<<pieces / 128, 128, 0, stream>>>(j); break;
+  }
   return launched();
 }
 

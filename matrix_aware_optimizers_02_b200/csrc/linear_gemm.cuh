@@ -12,12 +12,13 @@
 //   warps 2-9  epilogue, two per tensor-memory lane quarter, half of the columns each.
 // Two accumulators let an item's epilogue overlap the next item's MMAs.
 //
-// Tiles.  PAIR: 256 x 256 per CTA pair (tcgen05.mma.cta_group::2); each CTA loads 128 rows
-// of A and 128 of B's 256, 64 operand bytes per clock of tensor work against 96 for a
-// one-CTA 128 x 256 tile, which leaves shared memory room to refill.  One CTA: 128 x 128,
-// for products whose 256 x 256 tiles would leave most SMs idle.  K is cut into slices when
-// even those are too few: each slice leaves fp32 partial sums in the workspace and a second
-// kernel joins them in slice order and runs the same epilogue.
+// Tiles.  PAIR: 256 x BN per CTA pair (tcgen05.mma.cta_group::2); each CTA loads 128 rows
+// of A and half of B's BN.  BN = 256 streams 64 operand bytes per clock of tensor work, which
+// leaves shared memory room to refill; BN = 128 is for products whose 256 x 256 tiles leave
+// SMs idle.  One CTA: 128 x 128, for products of up to 128 rows.
+// The tiles behind the last full wave (all of them, where there are few) may be cut into K
+// slices: each slice leaves its fp32 sums of the tile in the workspace, and a second kernel
+// joins them in slice order and runs the same epilogue.
 //
 // Order.  Tiles run in bands of kBandRows tile rows, column by column inside a band, so the
 // tiles that are in flight together share few operand rows and columns in L2.
@@ -61,12 +62,13 @@ struct LinEpilogue {
 struct LinParams {
   CUtensorMap mapA, mapB;
   LinEpilogue e;
-  float* part;  // [slice][M][N] partial sums when slices > 1
+  float* part;  // [slice][tail tile][BM][BN]: sums of the sliced tiles
   int tiles_m, tiles_n;
-  int items;  // tiles * slices
+  int full;          // tiles [0, full) are whole items, the tail's come as `slices` items each
   int slices;
-  int nk;     // k-blocks of 64
-  int slice_blocks;
+  int items;
+  int nk;            // k-blocks of 64
+  int slice_blocks;  // k-blocks per slice
 };
 
 // ------------------------------------------------------------------ epilogue
@@ -179,15 +181,16 @@ __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int 
 }
 
 // ------------------------------------------------------------------ kernel
-template <bool PAIR>
+template <bool PAIR, int BN_>
 struct LinCfg {
   static constexpr int BM = PAIR ? 256 : 128;  // tile rows (128 per CTA)
-  static constexpr int BN = PAIR ? 256 : 128;  // tile columns
+  static constexpr int BN = BN_;               // tile columns
+  static constexpr int BL = PAIR ? BN / 2 : BN;  // B rows loaded by a CTA
   static constexpr int BK = 64;
   static constexpr int A_TILE = 128 * 128;  // bytes: 128 rows of 64 elements per CTA
-  static constexpr int B_TILE = 128 * 128;  // PAIR: half of B's rows per CTA
+  static constexpr int B_TILE = BL * 128;
   static constexpr int STAGE_BYTES = A_TILE + B_TILE;
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = STAGE_BYTES > 24 * 1024 ? 6 : 8;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 8;
@@ -195,33 +198,45 @@ struct LinCfg {
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
 };
 
+// Tile -> first row and column: bands of kBandRows tile rows, column by column.
+__host__ __device__ __forceinline__ void lin_tile(int tile, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int band = tile / (kBandRows * tiles_n);
+  const int first = band * kBandRows;
+  const int rows = tiles_m - first < kBandRows ? tiles_m - first : kBandRows;
+  const int r = tile - band * kBandRows * tiles_n;
+  tn = r / rows;
+  tm = first + r - tn * rows;
+}
+
 struct LinItem {
   int m0, n0;    // first row / column of the tile
   int kb0, kb1;  // its k-blocks
-  int slice;
+  int part;      // index of its sums in the workspace, or -1: a whole tile
 };
 
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ LinItem lin_item(const LinParams& p, int item) {
-  using Cfg = LinCfg<PAIR>;
-  const int tiles = p.tiles_m * p.tiles_n;
   LinItem t;
-  t.slice = item / tiles;
-  const int tile = item - t.slice * tiles;
-  const int band = tile / (kBandRows * p.tiles_n);
-  const int first = band * kBandRows;
-  const int rows = min(kBandRows, p.tiles_m - first);
-  const int r = tile - band * kBandRows * p.tiles_n;
-  const int c = r / rows;
-  t.n0 = c * Cfg::BN;
-  t.m0 = (first + r - c * rows) * Cfg::BM;
-  t.kb0 = t.slice * p.slice_blocks;
-  t.kb1 = min(p.nk, t.kb0 + p.slice_blocks);
+  int tile = item, slice = 0;
+  t.part = -1;
+  t.kb0 = 0, t.kb1 = p.nk;
+  if (item >= p.full && p.slices > 1) {
+    const int tail = p.tiles_m * p.tiles_n - p.full;
+    t.part = item - p.full;
+    slice = t.part / tail;
+    tile = p.full + t.part - slice * tail;
+    t.kb0 = slice * p.slice_blocks;
+    t.kb1 = min(p.nk, t.kb0 + p.slice_blocks);
+  }
+  int tm, tn;
+  lin_tile(tile, p.tiles_m, p.tiles_n, tm, tn);
+  t.m0 = tm * Cfg::BM;
+  t.n0 = tn * Cfg::BN;
   return t;
 }
 
-// One operand's share of a stage: 128 rows (K-major) or 128 columns of 64 K rows (MN-major).
-template <bool PAIR, int MN_MAJOR>
+// One operand's share of a stage: R rows (K-major) or R columns of 64 K rows (MN-major).
+template <bool PAIR, int MN_MAJOR, int R>
 __device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t bar_lead,
                                          int k0, int mn0) {
   if constexpr (!MN_MAJOR) {
@@ -229,16 +244,16 @@ __device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* map, u
     else tma_load_3d(dst, map, bar, k0, mn0, 0);
   } else {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < R / 64; ++c) {
       if constexpr (PAIR) tma_load_3d_pair(dst + c * 64 * 128, map, bar_lead, mn0 + c * 64, k0, 0);
       else tma_load_3d(dst + c * 64 * 128, map, bar, mn0 + c * 64, k0, 0);
     }
   }
 }
 
-template <class T, int KIND, int A_MN, int B_MN, bool PAIR>
+template <class T, int KIND, int A_MN, int B_MN, bool PAIR, int BN>
 __device__ __forceinline__ void lin_body(const LinParams& p) {
-  using Cfg = LinCfg<PAIR>;
+  using Cfg = LinCfg<PAIR, BN>;
   constexpr int STAGES = Cfg::STAGES, BK = Cfg::BK;
   constexpr uint32_t IDESC = make_idesc(Elem<T>::kDtype == MAO_BF16 ? 1u : 0u, A_MN, B_MN, Cfg::BM, Cfg::BN);
   constexpr int FOLD = KIND == LIN_GRAD32 ? kFoldBlocks : (1 << 30);  // k-blocks per accumulation
@@ -305,7 +320,7 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
       int it = 0;
       bool ok = true;
       for (int item = worker; item < p.items && ok; item += workers) {
-        const LinItem t = lin_item<PAIR>(p, item);
+        const LinItem t = lin_item<Cfg>(p, item);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1;
@@ -321,8 +336,9 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
           } else {
             mbar_arrive_expect_tx(&full_bar[s], Cfg::STAGE_BYTES);
           }
-          lin_load<PAIR, A_MN>(st, &p.mapA, &full_bar[s], lead, kb * BK, t.m0 + 128 * (int)rank);
-          lin_load<PAIR, B_MN>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK, t.n0 + 128 * (int)rank);
+          lin_load<PAIR, A_MN, 128>(st, &p.mapA, &full_bar[s], lead, kb * BK, t.m0 + 128 * (int)rank);
+          lin_load<PAIR, B_MN, Cfg::BL>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK,
+                                        t.n0 + Cfg::BL * (int)rank);
         }
       }
       prod_it_sh = it;
@@ -333,7 +349,7 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
       int it = 0, used = 0;
       bool ok = true;
       for (int item = worker; item < p.items && ok; item += workers) {
-        const LinItem t = lin_item<PAIR>(p, item);
+        const LinItem t = lin_item<Cfg>(p, item);
         for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += FOLD) {
           const int c1 = (t.kb1 - c0 > FOLD) ? c0 + FOLD : t.kb1;
           const int acc = used & 1;
@@ -356,7 +372,7 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
             const uint32_t b_base = a_base + Cfg::A_TILE;
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
-              const uint64_t ad = operand_desc<A_MN, 128, 2>(a_base, k), bd = operand_desc<B_MN, 128, 2>(b_base, k);
+              const uint64_t ad = operand_desc<A_MN, 128, 2>(a_base, k), bd = operand_desc<B_MN, Cfg::BL, 2>(b_base, k);
               const uint32_t accum = (kb > c0 || k > 0) ? 1u : 0u;
               if constexpr (PAIR) umma_f16_pair(d_tmem, ad, bd, IDESC, accum);
               else umma_f16(d_tmem, ad, bd, IDESC, accum);
@@ -388,25 +404,16 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
     int used = 0;
     bool ok = true;
     for (int item = worker; item < p.items && ok; item += workers) {
-      const LinItem t = lin_item<PAIR>(p, item);
+      const LinItem t = lin_item<Cfg>(p, item);
       const int row = t.m0 + 128 * (int)rank + q * 32 + lane;
       const int col = t.n0 + cb;
-      // what a 32-column chunk becomes: partial sums of a K slice, or the result
-      auto finish = [&](int c, float* v) {
-        if (p.slices > 1) {
-          const int n = min(32, p.e.N - c);
-          if (row < p.e.M && n > 0) {
-            float* o = p.part + ((long long)t.slice * p.e.M + row) * p.e.N + c;
-            if (n == 32) {
-              store_f32x32(o, v);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; j += 4)
-                if (j < n) *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-            }
-          }
+      // what a 32-column chunk becomes: sums of a K slice, or the result.  All of a sliced
+      // tile is stored, rows and columns behind the matrix too: they are zeros
+      auto finish = [&](int ch, float* v) {
+        if (t.part >= 0) {
+          store_f32x32(p.part + ((long long)t.part * Cfg::BM + (row - t.m0)) * Cfg::BN + cb + ch * 32, v);
         } else {
-          lin_epilogue<T, KIND>(p.e, row, c, v);
+          lin_epilogue<T, KIND>(p.e, row, col + ch * 32, v);
         }
       };
       if constexpr (KIND != LIN_GRAD32) {
@@ -426,7 +433,7 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(rr[j]);
-          finish(col + ch * 32, v);
+          finish(ch, v);
         }
         tc_fence_before();
         if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty_lead[acc]);
@@ -458,7 +465,7 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
         }
         if (!ok) break;
 #pragma unroll
-        for (int ch = 0; ch < COLS / 32; ++ch) finish(col + ch * 32, &run[ch * 32]);
+        for (int ch = 0; ch < COLS / 32; ++ch) finish(ch, &run[ch * 32]);
       }
     }
   }
@@ -485,40 +492,46 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
   }
 }
 
-template <class T, int KIND, int A_MN, int B_MN>
+template <class T, int KIND, int A_MN, int B_MN, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
     lin_pair_kernel(const __grid_constant__ LinParams p) {
-  lin_body<T, KIND, A_MN, B_MN, true>(p);
+  lin_body<T, KIND, A_MN, B_MN, true, BN>(p);
 }
 
 template <class T, int KIND, int A_MN, int B_MN>
 __global__ void __launch_bounds__(320, 1) lin_kernel(const __grid_constant__ LinParams p) {
-  lin_body<T, KIND, A_MN, B_MN, false>(p);
+  lin_body<T, KIND, A_MN, B_MN, false, 128>(p);
 }
 
-// Joins the K slices in slice order and runs the epilogue.  A thread owns 32 columns of a
-// row, as in the product kernel.
-template <class T, int KIND>
-__global__ void __launch_bounds__(128) lin_reduce_kernel(const LinEpilogue e, const float* __restrict__ part,
-                                                         int slices, int col_blocks, long long total) {
-  const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
-  if (i >= total) return;
-  const int row = (int)(i / col_blocks);
-  const int col = (int)(i - (long long)row * col_blocks) * 32;
-  const int n = min(32, e.N - col);
+// Joins the slices of the tail's tiles in slice order and runs the epilogue.  A thread owns
+// 32 columns of a row, as in the product kernel.
+struct LinJoin {
+  LinEpilogue e;
+  const float* part;
+  int tiles_m, tiles_n, full, slices;
+};
+template <class T, int KIND, int BM, int BN>
+__global__ void __launch_bounds__(128) lin_join_kernel(const LinJoin p) {
+  const int tail = p.tiles_m * p.tiles_n - p.full;
+  const int i = blockIdx.x * 128 + threadIdx.x;  // 32-column pieces of the tail's tiles
+  const int tile = i / (BM * BN / 32);
+  const int r = i - tile * (BM * BN / 32);
+  int tm, tn;
+  lin_tile(p.full + tile, p.tiles_m, p.tiles_n, tm, tn);
+  const int row = tm * BM + r / (BN / 32), col = tn * BN + (r % (BN / 32)) * 32;
+  if (row >= p.e.M || col >= p.e.N) return;
   float v[32];
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-  const float* s = part + (long long)row * e.N + col;
-  for (int k = 0; k < slices; ++k, s += (long long)e.M * e.N) {
+  const float* s = p.part + (long long)tile * BM * BN + r * 32;
+  for (int k = 0; k < p.slices; ++k, s += (long long)tail * BM * BN) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4)
-      if (j < n) {
-        const float4 a = *reinterpret_cast<const float4*>(s + j);
-        v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w;
-      }
+    for (int j = 0; j < 32; j += 4) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(s + j));
+      v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w;
+    }
   }
-  lin_epilogue<T, KIND>(e, row, col, v);
+  lin_epilogue<T, KIND>(p.e, row, col, v);
 }
 
 }  // namespace mao
