@@ -547,8 +547,9 @@ typedef enum {
   MAO_K_LINEAR = 32,         /* x W^T with its epilogue (tensor cores) */
   MAO_K_LINEAR_DX = 33,      /* dz W (tensor cores) */
   MAO_K_LINEAR_DW = 34,      /* dz^T x (tensor cores) */
-  MAO_K_ACT_BWD = 35,        /* dz = dy act'(z) with partial column sums (HBM) */
-  MAO_K_SLICE_REDUCE = 36    /* sum of a product's K slices, with its epilogue */
+  MAO_K_ACT_BWD = 35,        /* dz = dy act'(z) with partial column sums, x read back (HBM) */
+  MAO_K_SLICE_REDUCE = 36,   /* sum of a product's K slices, with its epilogue */
+  MAO_K_LINEAR_BWD = 37      /* dz W and dz^T x in one launch (tensor cores) */
 } mao_kernel_id;
 
 /* What one recorded launch was: its kernel and its algorithmic work (useful

@@ -118,7 +118,8 @@ KERNEL_NAMES = {1: "muon_prep", 2: "muon_scale", 3: "ns_gram", 4: "ns_poly", 5: 
                 17: "pc_sort", 18: "pc_qr", 19: "pc_rotate", 20: "pc_update", 21: "pc_panel", 22: "pc_chol",
                 23: "pc_qr_apply", 24: "pc_qr_reduce", 25: "pc_stats", 26: "mop_init", 27: "ckpt8",
                 28: "ckpt8_restore", 29: "layer_norm", 30: "layer_norm_bwd", 31: "col_reduce", 32: "linear",
-                33: "linear_dx", 34: "linear_dw", 35: "act_bwd", 36: "slice_reduce"}
+                33: "linear_dx", 34: "linear_dw", 35: "act_bwd", 36: "slice_reduce",
+                37: "linear_bwd"}
 
 # name -> (restype, argtypes)
 SIGNATURES = {

@@ -4,8 +4,11 @@
 // HBM-bound: dy 2 + z 2 (or 1 + 1/32 from a checkpoint) + dz 2 bytes per element.  A lane
 // owns 16 columns, a block 512 columns of a chunk of rows, each warp every eighth row; a
 // thread reads its next three rows ahead by cp.async.  Each chunk leaves one partial row of
-// column sums, joined in order by a second kernel (no atomics: the same bits every run).
+// column sums, which the product kernel joins in order (no atomics: the same bits every run).
+// Blocks behind those of this pass read the layer's input back from its checkpoint, so that
+// one launch prepares both operands.
 #include "act_bwd.h"
+#include "ckpt8.cuh"
 
 namespace mao {
 namespace {
@@ -18,6 +21,12 @@ struct ActArgs {
   float* part;  // [chunks][cols], or nullptr
   long long ld_dy, ld_z, ld_dz;
   int rows, cols, chunk;
+  int strips, blocks;  // column strips; blocks of this pass, the restore's come behind
+  // x read back from its checkpoint for the product that follows (xr == nullptr: not asked for)
+  CkptView xk;
+  void* xr;
+  long long ld_xr;
+  Steps xs;
 };
 
 constexpr int kCols = 16;    // columns per lane
@@ -33,13 +42,19 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const ActArgs a) {
   constexpr bool HAS = ACT != MAO_ACT_NONE;
   constexpr uint32_t kPiece = kThreads * 16;
   extern __shared__ __align__(16) uint8_t ring[];
+  launch_dependents();
+  if ((int)blockIdx.x >= a.blocks) {
+    restore_block<T, MAO_ACT_NONE>(a.xk, static_cast<T*>(a.xr), a.ld_xr, a.xs, (int)blockIdx.x - a.blocks);
+    return;
+  }
+  const int chunk_id = (int)blockIdx.x / a.strips, strip = (int)blockIdx.x - chunk_id * a.strips;
   const uint32_t slot = smem_u32(ring) + threadIdx.x * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // two vectors of 8 columns, 256 columns apart: neighbouring lanes read neighbouring 16 bytes
-  const int c = blockIdx.x * kStrip + lane * 8;
+  const int c = strip * kStrip + lane * 8;
   const int halves = c >= a.cols ? 0 : (c + 256 < a.cols ? 2 : 1);  // vectors inside the row
-  const long long r_end = min((long long)a.rows, ((long long)blockIdx.y + 1) * a.chunk);
-  const long long r_begin = (long long)blockIdx.y * a.chunk + warp;
+  const long long r_end = min((long long)a.rows, ((long long)chunk_id + 1) * a.chunk);
+  const long long r_begin = (long long)chunk_id * a.chunk + warp;
   const T* dy = static_cast<const T*>(a.dy);
   const T* z = static_cast<const T*>(a.z);
   auto fetch = [&](long long r, int stage) {
@@ -128,12 +143,12 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const ActArgs a) {
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) s += sh[w * kStrip + k];
-    if (blockIdx.x * kStrip + k < a.cols) a.part[(long long)blockIdx.y * a.cols + blockIdx.x * kStrip + k] = s;
+    if (strip * kStrip + k < a.cols) a.part[(long long)chunk_id * a.cols + strip * kStrip + k] = s;
   }
 }
 
 template <class T, int ACT, bool KEPT>
-mao_status run_one(const ActArgs& a, dim3 grid, cudaStream_t s) {
+mao_status run_one(const ActArgs& a, unsigned grid, cudaStream_t s) {
   constexpr int smem = kStages * kSlot<ACT, KEPT> * kThreads;  // at least the 16 KB of the joined sums
   static_assert(smem >= 8 * kStrip * (int)sizeof(float), "the joined sums use the ring's memory");
   static std::atomic<bool> done[64];
@@ -143,7 +158,7 @@ mao_status run_one(const ActArgs& a, dim3 grid, cudaStream_t s) {
 }
 
 template <class T, bool KEPT>
-mao_status run(const ActArgs& a, int act, dim3 grid, cudaStream_t s) {
+mao_status run(const ActArgs& a, int act, unsigned grid, cudaStream_t s) {
   switch (act) {
     case MAO_ACT_NONE: return run_one<T, MAO_ACT_NONE, false>(a, grid, s);
     case MAO_ACT_RELU: return run_one<T, MAO_ACT_RELU, KEPT>(a, grid, s);
@@ -165,17 +180,29 @@ int act_bwd_chunk(int rows, int cols) {
   return (rows + chunks - 1) / chunks;
 }
 
-mao_status act_bwd_launch(const void* dy, long long ld_dy, const void* z, long long ld_z, const CkptView& k, bool kept,
-                          int act, int dtype, int rows, int cols, void* dz, long long ld_dz, float* part,
-                          cudaStream_t stream) {
+mao_status act_bwd_launch(const ActBwd& b, int dtype, cudaStream_t stream) {
   ActArgs a;
-  a.dy = dy, a.z = z, a.k = k, a.dz = dz, a.part = part;
-  a.ld_dy = ld_dy, a.ld_z = ld_z, a.ld_dz = ld_dz;
-  a.rows = rows, a.cols = cols;
-  a.chunk = act_bwd_chunk(rows, cols);
-  const dim3 grid((cols + kStrip - 1) / kStrip, (rows + a.chunk - 1) / a.chunk);
+  a.dy = b.dy, a.z = b.z, a.k = b.zk, a.dz = b.dz, a.part = b.part;
+  a.ld_dy = b.ld_dy, a.ld_z = b.ld_z, a.ld_dz = b.ld_dz;
+  a.rows = b.rows, a.cols = b.cols;
+  a.chunk = act_bwd_chunk(b.rows, b.cols);
+  a.strips = (b.cols + kStrip - 1) / kStrip;
+  const bool sums = b.dz != nullptr || b.part != nullptr;
+  a.blocks = sums ? a.strips * ((b.rows + a.chunk - 1) / a.chunk) : 0;
+  a.xk = b.xk, a.xr = b.xr, a.ld_xr = b.x_cols;
+  unsigned grid = (unsigned)a.blocks;
+  if (b.xr != nullptr) {
+    DeviceInfo* dev = nullptr;
+    MAO_TRY(device_info(&dev));
+    grid += steps_of(b.rows, b.x_cols / 8, dev->sm_count, &a.xs);
+  }
+  if (grid == 0) return MAO_OK;
+  const bool kept = b.z == nullptr;
+  const int act = sums ? b.act : MAO_ACT_NONE;
   const double z_bytes = act == MAO_ACT_NONE ? 0.0 : (kept ? 1.0 + 1.0 / 32 : 2.0);
-  LaunchScope ls(stream, MAO_K_ACT_BWD, 0.0, (double)rows * cols * (2.0 + z_bytes + (dz ? 2.0 : 0.0)));
+  LaunchScope ls(stream, MAO_K_ACT_BWD, 0.0,
+                 (sums ? (double)b.rows * b.cols * (2.0 + z_bytes + (b.dz ? 2.0 : 0.0)) : 0.0) +
+                     (b.xr ? (double)b.rows * b.x_cols * (3.0 + 1.0 / 32) : 0.0));
   if (dtype == MAO_BF16)
     return kept ? run<__nv_bfloat16, true>(a, act, grid, stream) : run<__nv_bfloat16, false>(a, act, grid, stream);
   return kept ? run<__half, true>(a, act, grid, stream) : run<__half, false>(a, act, grid, stream);

@@ -8,9 +8,22 @@ namespace mao {
 // Rows per chunk; the pass writes ceil(rows / chunk) partial rows of column sums.
 int act_bwd_chunk(int rows, int cols);
 
-// rows, cols >= 1; dz == nullptr: column sums only; part == nullptr: no column sums.
-mao_status act_bwd_launch(const void* dy, long long ld_dy, const void* z, long long ld_z, const CkptView& k, bool kept,
-                          int act, int dtype, int rows, int cols, void* dz, long long ld_dz, float* part,
-                          cudaStream_t stream);
+struct ActBwd {
+  const void* dy;
+  long long ld_dy;
+  const void* z;  // nullptr: read zk
+  long long ld_z;
+  CkptView zk;
+  int act;
+  int rows, cols;  // of dy; rows >= 1
+  void* dz;        // nullptr: not written (no activation: dz is dy)
+  long long ld_dz;
+  float* part;     // partial column sums of dz, or nullptr
+  CkptView xk;     // read back to xr (rows x x_cols, dense), unless that is nullptr
+  void* xr;
+  int x_cols;
+};
+
+mao_status act_bwd_launch(const ActBwd& b, int dtype, cudaStream_t stream);
 
 }  // namespace mao

@@ -4,42 +4,19 @@
 // Both passes are HBM-bound: a 16-bit element costs 2 + 1 + 1/32 bytes either way.  A lane
 // owns 8 columns (16 bytes of a 16-bit type), 4 lanes a block of 32, whose largest magnitude
 // takes two shuffles; a thread keeps kUnroll vectors in flight.
+#include "ckpt8.cuh"
 #include "layer_host.h"
 
 namespace mao {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
-
-// A thread's walk over vectors of 8: a block takes tiles of kUnroll * kThreads consecutive
-// vectors, gridDim.x tiles apart, a thread kUnroll of each, kThreads apart.  One division at
-// the start, then additions: (row, vector) moves by (dr, dv) inside a tile and by (tr, tv) to
-// the next one (a division per vector made the read-back issue-bound: 133 instructions each).
-struct Steps {
-  long long total;  // vectors
-  int rows, vpr, dr, dv, tr, tv;
-};
-struct Walk {
-  long long row;
-  int v;
-  __device__ __forceinline__ Walk(const Steps& s) {
-    const uint32_t i = blockIdx.x * (kThreads * kUnroll) + threadIdx.x;  // below 2^31
-    const uint32_t r = i / (uint32_t)s.vpr;
-    row = r;
-    v = (int)(i - r * (uint32_t)s.vpr);
-  }
-  __device__ __forceinline__ void move(int dr, int dv, int vpr) {
-    row += dr;
-    v += dv;
-    if (v >= vpr) v -= vpr, ++row;
-  }
-};
+constexpr int kThreads = kCkptThreads;
+constexpr int kUnroll = kCkptUnroll;
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x, long long ld_x, CkptView k, Steps st,
                                                          int cols) {
-  Walk at(st);
+  Walk at(st, blockIdx.x);
   const long long tile = kThreads * kUnroll;
   // uniform over the block: lanes behind the last vector take part in the shuffles
   for (long long i = blockIdx.x * tile; i < st.total; i += gridDim.x * tile) {
@@ -67,51 +44,9 @@ __global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x
 
 template <class T, int ACT>
 __global__ void __launch_bounds__(kThreads) restore_kernel(CkptView k, T* __restrict__ y, long long ld_y, Steps st) {
-  Walk at(st);
-  while (at.row < st.rows) {
-    CkptVec8 v[kUnroll];
-    long long row[kUnroll];
-    int col[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      row[u] = at.row;
-      col[u] = at.v * 8;
-      if (at.row < st.rows) v[u].load(k, at.row, col[u]);
-      at.move(st.dr, st.dv, st.vpr);
-    }
-    at.move(st.tr, st.tv, st.vpr);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (row[u] >= st.rows) break;
-      f2 f[4];
-      v[u].get(f);
-      Vec8<T> o;
-      if constexpr (ACT == MAO_ACT_NONE) {
-        o.set_exact(f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = act_value<ACT, sizeof(T) == 4>(f[j]);
-        o.set(f);
-      }
-      o.store(y + row[u] * ld_y + col[u]);
-    }
-  }
+  restore_block<T, ACT>(k, y, ld_y, st, blockIdx.x);
 }
 
-// One wave of blocks walks everything; never more blocks than vectors ask for.
-unsigned steps_of(int rows, int vpr, int sms, Steps* s) {
-  s->total = (long long)rows * vpr;
-  s->rows = rows;
-  s->vpr = vpr;
-  const long long tile = kThreads * kUnroll;
-  const long long grid = std::min<long long>((s->total + tile - 1) / tile, 8ll * sms);
-  s->dr = kThreads / vpr;
-  s->dv = kThreads % vpr;
-  const long long rest = (grid - 1) * tile;  // a tile's kUnroll moves have covered the first
-  s->tr = (int)(rest / vpr);
-  s->tv = (int)(rest % vpr);
-  return (unsigned)grid;
-}
 template <class T>
 mao_status pack(const void* x, long long ld_x, const CkptView& k, int rows, int cols, cudaStream_t stream) {
   const int vpr = ckpt_blocks(cols) * 4;

@@ -45,12 +45,30 @@ mao_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
   return MAO_OK;
 }
 
+// Launch as a programmatic dependent of the kernel before it in the stream, which must be one
+// of this call's: launch latency and set-up overlap that kernel's end.  The kernel calls
+// wait_for_previous() before it touches global memory.
+template <class... P, class... A>
+mao_status launch_dependent(void (*kern)(P...), dim3 grid, int block, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, args...) == cudaSuccess ? MAO_OK : MAO_ERR_CUDA;
+}
+
 // y = act(value of c); arguments checked by the caller, rows >= 1
 mao_status restore_launch(const CkptView& c, int rows, int cols, int act, void* y, int dtype, long long ld_y,
                           cudaStream_t stream);
 
-// out0[col] = sum over parts of part[p * cols + col], in a fixed order; out1 likewise of the
-// parts * cols values behind.  Either may be nullptr.
-mao_status col_reduce_launch(const float* part, int parts, int cols, float* out0, float* out1, cudaStream_t stream);
+// out[col] = sum over parts of part[p * cols + col], in a fixed order; follows the kernel that
+// wrote the parts
+mao_status col_sum_launch(const float* part, int parts, int cols, float* out, cudaStream_t stream);
 
 }  // namespace mao

@@ -185,6 +185,14 @@ __device__ __forceinline__ void load_param8(const void* p, bool f32, long long i
   }
 }
 
+// ------------------------------------------------------------------ dependent launches
+// A kernel launched as a programmatic dependent (launch_dependent in layer_host.h) may start
+// while the kernel before it in the stream still runs: it waits here before it touches global
+// memory, and with that for everything before, since every kernel of a chain waits.  The
+// kernel before says when the dependents may be scheduled.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ asynchronous loads
 // A thread's own ring in shared memory: cp.async of 16 (or 8) bytes that only the issuing
 // thread reads back, so no barrier orders them, only its own wait.  With ok false nothing is

@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
   };
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) fetch(row0 + d * step, d);
+  launch_dependents();  // the column reduction's blocks, as this kernel's end
   Small now, next = fetch_small(row0), after = fetch_small(row0 + step);
   f2 w[VPT][4], dw[VPT][4], db[VPT][4];
 #pragma unroll
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
 __global__ void __launch_bounds__(1024) col_reduce_kernel(const float* __restrict__ part, int parts, int cols,
                                                           float* __restrict__ out0, float* __restrict__ out1) {
   __shared__ float sh[32][33];
+  wait_for_previous();
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float* out = blockIdx.y == 0 ? out0 : out1;
@@ -510,12 +512,18 @@ size_t bwd_bytes(const mao_layer_norm_backward_args* a, int sms) {
   return sizeof(float) * 2 * (size_t)bwd_blocks(a->rows, a->cols, sms) * (size_t)a->cols;
 }
 
-}  // namespace
-
+// out0[col] = sum over parts of part[p * cols + col]; out1 likewise of the parts * cols values
+// behind.  Either may be nullptr.
 mao_status col_reduce_launch(const float* part, int parts, int cols, float* out0, float* out1, cudaStream_t stream) {
   LaunchScope ls(stream, MAO_K_COL_REDUCE, 0.0, 4.0 * (double)parts * cols * (out1 ? 2 : 1));
-  col_reduce_kernel<<<dim3((cols + 31) / 32, out1 ? 2 : 1), 1024, 0, stream>>>(part, parts, cols, out0, out1);
-  return launched();
+  return launch_dependent(col_reduce_kernel, dim3((cols + 31) / 32, out1 ? 2 : 1), 1024, 0, stream, part, parts, cols,
+                          out0, out1);
+}
+
+}  // namespace
+
+mao_status col_sum_launch(const float* part, int parts, int cols, float* out, cudaStream_t stream) {
+  return col_reduce_launch(part, parts, cols, out, nullptr, stream);
 }
 
 }  // namespace mao

@@ -9,44 +9,96 @@ namespace {
 // ------------------------------------------------------------------ plan
 enum LinTile : int { TILE_PAIR256 = 0, TILE_PAIR128 = 1, TILE_ONE = 2 };
 constexpr int kTileM[3] = {256, 256, 128}, kTileN[3] = {256, 128, 128};
+constexpr int kPlanSms = 148;
 
+struct Shape {
+  long long M, N, K;
+};
 struct LinPlan {
-  int tile = TILE_ONE;
   int tiles_m = 0, tiles_n = 0, nk = 0, full = 0, slices = 1, slice_blocks = 0;
   int items = 0;
   size_t part_bytes = 0;
 };
+struct LinPlans {
+  int tile = TILE_ONE;
+  LinPlan p[2];
+  size_t part_bytes() const { return p[0].part_bytes + p[1].part_bytes; }
+};
 
-// Tiles and K slices of an M x N x K product, from its sizes alone (and so the same on
-// every device and in the workspace query): the cheapest by estimated clocks.
-constexpr int kPlanSms = 148;
-
-bool plan_of(long long M, long long N, long long K, LinPlan* out) {
-  // clocks of a k-block of 64, of the last epilogue, and of a join of the slices
-  constexpr double kBlock[3] = {530.0, 400.0, 700.0}, kTail[3] = {5000.0, 4000.0, 4000.0};
-  constexpr double kJoin = 7000.0, kJoinBytes = 2000.0;  // launch; bytes per clock
-  const long long nk = (K + 63) / 64;
+// Tiles and K slices of one product, or of two that share a launch (the longer K first), from
+// their sizes alone (and so the same on every device and in the workspace query): the
+// cheapest by estimated nanoseconds.
+bool plan_of(const Shape* q, int n, LinPlans* out) {
+  // a k-block of 64; set-up, first loads and last epilogue; the joining kernel
+  constexpr double kBlock[3] = {385.0, 300.0, 320.0}, kFixed[3] = {6500.0, 5500.0, 5000.0};
+  constexpr double kJoin = 3500.0, kJoinBytes = 4000.0;  // its launch; bytes per ns, written and read
   double best = 1e300;
   for (int t = 0; t < 3; ++t) {
-    const long long tm = (M + kTileM[t] - 1) / kTileM[t], tn = (N + kTileN[t] - 1) / kTileN[t], tiles = tm * tn;
-    if (tiles > (1ll << 27)) continue;
     const long long workers = t == TILE_ONE ? kPlanSms : kPlanSms / 2;
-    const long long waves = tiles / workers, rest = tiles - waves * workers;
-    for (int s = 1; s <= 16; ++s) {
-      const long long sb = (nk + s - 1) / s;
-      if (s > 1 && (rest == 0 || sb < 4 || (nk + sb - 1) / sb != s)) break;
-      const long long rounds = (rest * s + workers - 1) / workers;
-      double cost = (double)(waves * nk + rounds * sb) * kBlock[t] + kTail[t];
-      const double bytes = s > 1 ? 4.0 * s * (double)rest * kTileM[t] * kTileN[t] : 0.0;
-      if (s > 1) cost += kJoin + 2.0 * bytes / kJoinBytes;
-      if (cost < best) {
-        best = cost;
-        out->tile = t;
-        out->tiles_m = (int)tm, out->tiles_n = (int)tn, out->nk = (int)nk;
-        out->full = (int)(s > 1 ? tiles - rest : tiles);
-        out->slices = s, out->slice_blocks = (int)sb;
-        out->items = out->full + (int)(tiles - out->full) * s;
-        out->part_bytes = (size_t)bytes;
+    LinPlans c;
+    c.tile = t;
+    long long tiles[2] = {0, 0};
+    bool fits = true;
+    for (int i = 0; i < n; ++i) {
+      const long long tm = (q[i].M + kTileM[t] - 1) / kTileM[t], tn = (q[i].N + kTileN[t] - 1) / kTileN[t];
+      tiles[i] = tm * tn;
+      fits = fits && tiles[i] <= (1ll << 27);
+      c.p[i].tiles_m = (int)tm, c.p[i].tiles_n = (int)tn;
+      c.p[i].nk = (int)((q[i].K + 63) / 64);
+    }
+    if (!fits) continue;
+    // cut[i]: tiles of problem i behind the last full wave of the launch; slices for each
+    const long long rest = (tiles[0] + tiles[1]) % workers;
+    const long long cut[2] = {n == 1 ? rest : std::max(0ll, rest - tiles[1]), n == 1 ? 0 : std::min(rest, tiles[1])};
+    for (int s0 = 1; s0 <= 16; ++s0) {
+      for (int s1 = 1; s1 <= 16; ++s1) {
+        const int s[2] = {s0, s1};
+        // whole items of every problem, then the slices, dealt in turn to the workers: the
+        // length of the longest is estimated by the mean plus the longest item
+        double sum = 0.0, longest = 0.0, bytes = 0.0;
+        bool ok = true;
+        for (int i = 0; i < 2; ++i) {
+          LinPlan& p = c.p[i];
+          const bool sliced = s[i] > 1;
+          if (i >= n || cut[i] == 0 || p.nk < 8) {
+            if (sliced) ok = false;
+            if (i >= n) continue;
+          }
+          p.slices = s[i];
+          p.slice_blocks = (p.nk + s[i] - 1) / s[i];
+          if (sliced && (p.slice_blocks < 4 || (p.nk + p.slice_blocks - 1) / p.slice_blocks != s[i])) ok = false;
+          if (!ok) break;
+          p.full = (int)(sliced ? tiles[i] - cut[i] : tiles[i]);
+          p.items = p.full + (int)(tiles[i] - p.full) * p.slices;
+          p.part_bytes = sliced ? 4ull * p.slices * (size_t)cut[i] * kTileM[t] * kTileN[t] : 0;
+          sum += (double)tiles[i] * p.nk;
+          bytes += (double)p.part_bytes;
+        }
+        if (!ok) continue;
+        // deal the items out: worker w gets items w, w + workers, ...
+        const long long n0 = c.p[0].items, n1 = n > 1 ? c.p[1].items : 0, all = n0 + n1;
+        const long long per = all / workers, left = all - per * workers;
+        auto len = [&](long long item) -> double {
+          const LinPlan& p = item < n0 ? c.p[0] : c.p[1];
+          const long long k = item < n0 ? item : item - n0;
+          return k < p.full ? p.nk : p.slice_blocks;
+        };
+        // the first, last and boundary workers hold the extremes
+        const long long probe[4] = {0, left > 0 ? left - 1 : workers - 1, n0 % workers, (c.p[0].full) % workers};
+        for (long long w : probe) {
+          double l = 0.0;
+          if (all <= 64 * workers) {
+            for (long long i = w; i < all; i += workers) l += len(i);
+          } else {
+            l = (double)(sum / workers) + len(all - 1);
+          }
+          longest = std::max(longest, l);
+        }
+        const double cost = longest * kBlock[t] + kFixed[t] + (bytes > 0 ? kJoin + 2.0 * bytes / kJoinBytes : 0.0);
+        if (cost < best) {
+          best = cost;
+          *out = c;
+        }
       }
     }
   }
@@ -54,16 +106,19 @@ bool plan_of(long long M, long long N, long long K, LinPlan* out) {
 }
 
 // ------------------------------------------------------------------ launch
-template <class T, int KIND, int A_MN, int B_MN, bool PAIR, int BN>
-mao_status launch_product(const LinParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+template <class T, bool FORWARD, bool PAIR, int BN>
+mao_status launch_product(const LinParams<FORWARD ? 1 : 2>& p, int items, bool dependent, const DeviceInfo& dev,
+                          cudaStream_t stream) {
   using Cfg = LinCfg<PAIR, BN>;
-  void (*kern)(LinParams);
-  if constexpr (PAIR) kern = lin_pair_kernel<T, KIND, A_MN, B_MN, BN>;
-  else kern = lin_kernel<T, KIND, A_MN, B_MN>;
+  void (*kern)(LinParams<FORWARD ? 1 : 2>);
+  if constexpr (PAIR) kern = lin_pair_kernel<T, FORWARD, BN>;
+  else kern = lin_kernel<T, FORWARD>;
   static std::atomic<bool> done[64];
   MAO_TRY(allow_smem(kern, Cfg::SMEM_BYTES, done));
-  const int workers = std::min(p.items, PAIR ? dev.sm_count / 2 : dev.sm_count);
-  kern<<<PAIR ? 2 * workers : workers, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(p);
+  const int workers = std::min(items, PAIR ? dev.sm_count / 2 : dev.sm_count);
+  const int grid = PAIR ? 2 * workers : workers;
+  if (dependent) return launch_dependent(kern, dim3(grid), Cfg::THREADS, Cfg::SMEM_BYTES, stream, p);
+  kern<<<grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(p);
   return launched();
 }
 
@@ -79,45 +134,78 @@ mao_status encode(CUtensorMap* map, int dtype, const Operand& o, bool mn, int bo
                    mn ? 64 : box_rows);
 }
 
-template <class T, int KIND, int A_MN, int B_MN>
-mao_status product(const Operand& A, const Operand& B, const LinEpilogue& e, const LinPlan& plan, float* part,
-                   int kernel_id, double bytes, cudaStream_t stream) {
+// One product of a launch: out = A B^T with the stored operands as described.
+struct Product {
+  Operand A, B;
+  int a_mn;  // A's major
+  LinEpilogue e;
+  Shape shape() const { return Shape{e.M, e.N, a_mn ? A.rows : A.inner}; }
+};
+
+// One or two products in one launch, then the joining of their slices.  dependent: a kernel of
+// this call comes before in the stream.
+template <class T, bool FORWARD>
+mao_status products(const Product* q, int n, const LinPlans& plans, const LinColSum& sum, float* part, int kernel_id,
+                    double bytes, bool dependent, cudaStream_t stream) {
+  constexpr int NP = FORWARD ? 1 : 2;
   DeviceInfo* dev = nullptr;
   MAO_TRY(device_info(&dev));
-  LinParams p;
-  MAO_TRY(encode(&p.mapA, Elem<T>::kDtype, A, A_MN, 128));
-  MAO_TRY(encode(&p.mapB, Elem<T>::kDtype, B, B_MN, plan.tile == TILE_PAIR128 ? 64 : 128));
-  p.e = e;
-  p.part = part;
-  p.tiles_m = plan.tiles_m, p.tiles_n = plan.tiles_n;
-  p.full = plan.full, p.slices = plan.slices, p.slice_blocks = plan.slice_blocks;
-  p.nk = plan.nk, p.items = plan.items;
-  const long long K = A_MN ? A.rows : A.inner;
-  {
-    LaunchScope ls(stream, kernel_id, 2.0 * e.M * (double)e.N * (double)K, bytes);
-    switch (plan.tile) {
-      case TILE_PAIR256: MAO_TRY((launch_product<T, KIND, A_MN, B_MN, true, 256>(p, *dev, stream))); break;
-      case TILE_PAIR128: MAO_TRY((launch_product<T, KIND, A_MN, B_MN, true, 128>(p, *dev, stream))); break;
-      default: MAO_TRY((launch_product<T, KIND, A_MN, B_MN, false, 128>(p, *dev, stream))); break;
+  LinParams<NP> a;
+  LinJoins<NP> j;
+  std::memset(&a, 0, sizeof(a));
+  std::memset(&j, 0, sizeof(j));
+  a.sum = sum;
+  double flops = 0.0;
+  int items = 0, pieces = 0;
+  for (int i = 0; i < n; ++i) {
+    const LinPlan& c = plans.p[i];
+    LinProblem& p = a.p[i];
+    MAO_TRY(encode(&p.mapA, Elem<T>::kDtype, q[i].A, q[i].a_mn, 128));
+    MAO_TRY(encode(&p.mapB, Elem<T>::kDtype, q[i].B, !FORWARD, plans.tile == TILE_PAIR128 ? 64 : 128));
+    p.e = q[i].e;
+    p.part = part;
+    part += c.part_bytes / sizeof(float);
+    p.a_mn = q[i].a_mn;
+    p.tiles_m = c.tiles_m, p.tiles_n = c.tiles_n;
+    p.full = c.full, p.slices = c.slices, p.items = c.items;
+    p.nk = c.nk, p.slice_blocks = c.slice_blocks;
+    p.fold = p.e.kind == LIN_GRAD32 || p.e.k.q != nullptr ? kFoldBlocks : p.nk;
+    items += c.items;
+    const Shape s = q[i].shape();
+    flops += 2.0 * (double)s.M * (double)s.N * (double)s.K;
+    j.p[i] = LinJoin{p.e, p.part, c.tiles_m, c.tiles_n, c.full, c.slices};
+    if (c.slices > 1) {
+      // at most one wave of tiles: far below 2^31 pieces, a multiple of 128
+      const int k = (c.tiles_m * c.tiles_n - c.full) * (kTileM[plans.tile] * kTileN[plans.tile] / 32);
+      if (i == 0) j.pieces = k;
+      pieces += k;
     }
   }
-  if (plan.slices == 1) return MAO_OK;
-  const LinJoin j{e, part, plan.tiles_m, plan.tiles_n, plan.full, plan.slices};
-  // at most one wave of tiles: far below 2^31 pieces
-  const int pieces = (plan.tiles_m * plan.tiles_n - plan.full) * (kTileM[plan.tile] * kTileN[plan.tile] / 32);
-  LaunchScope ls(stream, MAO_K_SLICE_REDUCE, 0.0, (double)plan.part_bytes);
-  switch (plan.tile) {
-    case TILE_PAIR256: lin_join_kernel<T, KIND, 256, 256><<<pieces / 128, 128, 0, stream>>>(j); break;
-    case TILE_PAIR128: lin_join_kernel<T, KIND, 256, 128><<<pieces / 128, 128, 0, stream>>>(j); break;
-    default: lin_join_kernel<T, KIND, 128, 128><<<pieces / 128, 128, 0, stream>>>(j); break;
+  for (int i = n; i < NP; ++i) {  // an absent second problem has no items; its maps are only prefetched
+    a.p[i].mapA = a.p[0].mapA, a.p[i].mapB = a.p[0].mapB;
   }
-  return launched();
+  {
+    LaunchScope ls(stream, kernel_id, flops, bytes);
+    switch (plans.tile) {
+      case TILE_PAIR256: MAO_TRY((launch_product<T, FORWARD, true, 256>(a, items, dependent, *dev, stream))); break;
+      case TILE_PAIR128: MAO_TRY((launch_product<T, FORWARD, true, 128>(a, items, dependent, *dev, stream))); break;
+      default: MAO_TRY((launch_product<T, FORWARD, false, 128>(a, items, dependent, *dev, stream))); break;
+    }
+  }
+  if (pieces == 0) return MAO_OK;
+  LaunchScope ls(stream, MAO_K_SLICE_REDUCE, 0.0, (double)plans.part_bytes());
+  const dim3 grid(pieces / 128);
+  switch (plans.tile) {
+    case TILE_PAIR256: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 256>, grid, 128, 0, stream, j);
+    case TILE_PAIR128: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 128>, grid, 128, 0, stream, j);
+    default: return launch_dependent(lin_join_kernel<T, FORWARD, 128, 128>, grid, 128, 0, stream, j);
+  }
 }
 
-LinEpilogue epilogue(void* out, long long ld, int M, int N) {
+LinEpilogue epilogue(void* out, long long ld, int M, int N, int kind) {
   LinEpilogue e;
   std::memset(&e, 0, sizeof(e));
-  e.out = out, e.ld_out = ld, e.M = M, e.N = N;
+  e.out = out, e.ld_out = ld, e.M = M, e.N = N, e.kind = kind;
   return e;
 }
 
@@ -141,7 +229,10 @@ mao_status check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 struct BwdLayout {
-  LinPlan dx, dw;
+  LinPlans plans;       // of the products asked for, the longer K first
+  int products = 0;
+  bool dx_first = false;
+  int chunks = 0;       // partial rows of the bias gradient
   size_t dz = 0, x = 0, db = 0, part = 0, total = 0;
 };
 
@@ -156,70 +247,73 @@ mao_status backward_layout(const mao_linear_backward_args* a, BwdLayout* L) {
   if (a->dW && a->x == nullptr) L->x = cv.take(2 * rows * a->n);
   if (a->db) {
     const int chunk = act_bwd_chunk(a->rows, a->m);
-    L->db = cv.take(sizeof(float) * (size_t)((a->rows + chunk - 1) / chunk) * a->m);
+    L->chunks = (a->rows + chunk - 1) / chunk;
+    L->db = cv.take(sizeof(float) * (size_t)L->chunks * a->m);
   }
-  if (a->dx && !plan_of(a->rows, a->n, a->m, &L->dx)) return MAO_ERR_SHAPE;
-  if (a->dW && !plan_of(a->m, a->n, a->rows, &L->dw)) return MAO_ERR_SHAPE;
-  // one after the other on the stream: they share the slices' room
-  L->part = cv.take(std::max(L->dx.part_bytes, L->dw.part_bytes));
+  const Shape dx{a->rows, a->n, a->m}, dw{a->m, a->n, a->rows};
+  L->dx_first = a->dx && (!a->dW || a->m >= a->rows);
+  Shape q[2];
+  if (L->dx_first) q[L->products++] = dx;
+  if (a->dW) q[L->products++] = dw;
+  if (a->dx && !L->dx_first) q[L->products++] = dx;
+  if (L->products > 0 && !plan_of(q, L->products, &L->plans)) return MAO_ERR_SHAPE;
+  L->part = cv.take(L->plans.part_bytes());
   L->total = cv.total();
   return MAO_OK;
 }
 
 template <class T>
-mao_status forward(const mao_linear_args* a, const LinPlan& plan, float* part, cudaStream_t stream) {
-  LinEpilogue e = epilogue(a->y, a->ld_y, a->rows, a->m);
+mao_status forward(const mao_linear_args* a, const LinPlans& plans, float* part, cudaStream_t stream) {
+  LinEpilogue e = epilogue(a->y, a->ld_y, a->rows, a->m, LIN_FORWARD);
   e.bias = a->b, e.bias_f32 = a->b_dtype == MAO_F32;
   e.res = a->res, e.ld_res = a->ld_res;
   e.z = a->z, e.ld_z = a->ld_z;
   e.k = view(a->zc);
   e.act = a->act;
-  const Operand x{a->x, a->n, a->rows, a->ld_x}, W{a->W, a->n, a->m, a->n};
+  const Product q{{a->x, a->n, a->rows, a->ld_x}, {a->W, a->n, a->m, a->n}, 0, e};
   const double r = a->rows, n = a->n, m = a->m;
-  return product<T, LIN_FORWARD, 0, 0>(x, W, e, plan, part, MAO_K_LINEAR,
-                                       2.0 * (r * n + m * n + r * m) + (a->res ? 2.0 * r * m : 0.0) +
-                                           (a->z ? 2.0 * r * m : 0.0) + (a->zc.q ? r * m * (1.0 + 1.0 / 32) : 0.0),
-                                       stream);
+  return products<T, true>(&q, 1, plans, LinColSum{}, part, MAO_K_LINEAR,
+                           2.0 * (r * n + m * n + r * m) + (a->res ? 2.0 * r * m : 0.0) + (a->z ? 2.0 * r * m : 0.0) +
+                               (a->zc.q ? r * m * (1.0 + 1.0 / 32) : 0.0),
+                           false, stream);
 }
 
+// One elementwise launch (dz, the bias gradient's partial sums, x read back), then one launch
+// for both products, which also joins the bias gradient.
 template <class T>
 mao_status backward(const mao_linear_backward_args* a, const BwdLayout& L, uint8_t* ws, cudaStream_t stream) {
   const bool has_act = a->act != MAO_ACT_NONE;
-  const bool products = a->dx || a->dW;
-  const void* dz = a->dy;
-  long long ld_dz = a->ld_dy;
-  if ((has_act && products) || a->db) {
-    void* out = has_act && products ? ws + L.dz : nullptr;
-    float* part = a->db ? reinterpret_cast<float*>(ws + L.db) : nullptr;
-    MAO_TRY(act_bwd_launch(a->dy, a->ld_dy, a->z, a->ld_z, view(a->zc), a->z == nullptr, a->act, a->dtype, a->rows,
-                           a->m, out, a->m, part, stream));
-    if (out) dz = out, ld_dz = a->m;
-    if (a->db) {
-      const int chunk = act_bwd_chunk(a->rows, a->m);
-      MAO_TRY(col_reduce_launch(part, (a->rows + chunk - 1) / chunk, a->m, a->db, nullptr, stream));
-    }
-  }
-  float* part = reinterpret_cast<float*>(ws + L.part);
+  ActBwd b = {};
+  b.dy = a->dy, b.ld_dy = a->ld_dy;
+  b.z = a->z, b.ld_z = a->ld_z, b.zk = view(a->zc);
+  b.act = a->act;
+  b.rows = a->rows, b.cols = a->m;
+  if (has_act && L.products > 0) b.dz = ws + L.dz, b.ld_dz = a->m;
+  if (a->db) b.part = reinterpret_cast<float*>(ws + L.db);
+  if (a->dW && a->x == nullptr) b.xk = view(a->xc), b.xr = ws + L.x, b.x_cols = a->n;
+  const bool prepared = b.dz || b.part || b.xr;
+  if (prepared) MAO_TRY(act_bwd_launch(b, a->dtype, stream));
   const double r = a->rows, n = a->n, m = a->m;
-  const Operand Z{dz, a->m, a->rows, ld_dz};
-  if (a->dx) {
-    const LinEpilogue e = epilogue(a->dx, a->ld_dx, a->rows, a->n);
-    const Operand W{a->W, a->n, a->m, a->n};
-    MAO_TRY((product<T, LIN_STORE, 0, 1>(Z, W, e, L.dx, part, MAO_K_LINEAR_DX, 2.0 * (r * n + m * n + r * m), stream)));
+  if (L.products == 0) {
+    if (a->db) return col_sum_launch(b.part, L.chunks, a->m, a->db, stream);
+    return MAO_OK;
   }
-  if (a->dW) {
-    Operand X{a->x, a->n, a->rows, a->ld_x};
-    if (a->x == nullptr) {
-      MAO_TRY(restore_launch(view(a->xc), a->rows, a->n, MAO_ACT_NONE, ws + L.x, a->dtype, a->n, stream));
-      X.p = ws + L.x, X.ld = a->n;
-    }
-    LinEpilogue e = epilogue(a->dW, a->n, a->m, a->n);
-    e.accumulate = a->accumulate;
-    if (a->dw_dtype == MAO_F32)
-      return product<T, LIN_GRAD32, 1, 1>(Z, X, e, L.dw, part, MAO_K_LINEAR_DW, 2.0 * (r * n + r * m) + 4.0 * m * n, stream);
-    return product<T, LIN_STORE, 1, 1>(Z, X, e, L.dw, part, MAO_K_LINEAR_DW, 2.0 * (r * n + r * m + m * n), stream);
-  }
-  return MAO_OK;
+  const Operand Z = b.dz ? Operand{b.dz, a->m, a->rows, a->m} : Operand{a->dy, a->m, a->rows, a->ld_dy};
+  const Operand X = b.xr ? Operand{b.xr, a->n, a->rows, a->n} : Operand{a->x, a->n, a->rows, a->ld_x};
+  Product dx{Z, {a->W, a->n, a->m, a->n}, 0, epilogue(a->dx, a->ld_dx, a->rows, a->n, LIN_STORE)};
+  Product dw{Z, X, 1, epilogue(a->dW, a->n, a->m, a->n, a->dw_dtype == MAO_F32 ? LIN_GRAD32 : LIN_STORE)};
+  dw.e.accumulate = a->accumulate;
+  Product q[2];
+  int k = 0;
+  if (L.dx_first) q[k++] = dx;
+  if (a->dW) q[k++] = dw;
+  if (a->dx && !L.dx_first) q[k++] = dx;
+  const LinColSum sum{b.part, a->db, L.chunks, a->m};
+  const double dw_bytes = (a->dw_dtype == MAO_F32 ? 4.0 : 2.0) * m * n;
+  return products<T, false>(q, k, L.plans, sum, reinterpret_cast<float*>(ws + L.part),
+                            k == 2 ? MAO_K_LINEAR_BWD : (a->dx ? MAO_K_LINEAR_DX : MAO_K_LINEAR_DW),
+                            2.0 * r * m + (a->dx ? 2.0 * (m * n + r * n) : 0.0) + (a->dW ? 2.0 * r * n + dw_bytes : 0.0),
+                            prepared, stream);
 }
 
 }  // namespace
@@ -232,9 +326,10 @@ extern "C" mao_status mao_linear_workspace_size(const mao_linear_args* a, size_t
   MAO_TRY(check_sizes(a->dtype, a->rows, a->n, a->m));
   *bytes = 0;
   if (a->rows == 0) return MAO_OK;
-  LinPlan plan;
-  if (!plan_of(a->rows, a->m, a->n, &plan)) return MAO_ERR_SHAPE;
-  *bytes = align_up(plan.part_bytes, 256);
+  LinPlans plans;
+  const Shape q{a->rows, a->m, a->n};
+  if (!plan_of(&q, 1, &plans)) return MAO_ERR_SHAPE;
+  *bytes = align_up(plans.part_bytes(), 256);
   return MAO_OK;
 }
 
@@ -256,11 +351,12 @@ extern "C" mao_status mao_linear(const mao_linear_args* a, void* workspace, size
   DeviceInfo* dev = nullptr;
   MAO_TRY(device_info(&dev));
   if (a->rows == 0) return MAO_OK;
-  LinPlan plan;
-  if (!plan_of(a->rows, a->m, a->n, &plan)) return MAO_ERR_SHAPE;
+  LinPlans plans;
+  const Shape q{a->rows, a->m, a->n};
+  if (!plan_of(&q, 1, &plans)) return MAO_ERR_SHAPE;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   float* part = static_cast<float*>(workspace);
-  return a->dtype == MAO_BF16 ? forward<__nv_bfloat16>(a, plan, part, stream) : forward<__half>(a, plan, part, stream);
+  return a->dtype == MAO_BF16 ? forward<__nv_bfloat16>(a, plans, part, stream) : forward<__half>(a, plans, part, stream);
 }
 
 extern "C" mao_status mao_linear_backward_workspace_size(const mao_linear_backward_args* a, size_t* bytes) {

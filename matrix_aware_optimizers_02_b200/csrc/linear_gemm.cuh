@@ -6,11 +6,14 @@
 //   dW         dW = dz^T x                 A = dz (MN-major),    B = x (MN-major)
 //
 // One persistent kernel, one CTA per SM or one CTA pair per two SMs, walking work items
-// (output tile, K slice) with a static stride.  Warp roles (320 threads):
-//   warp 0     TMA producer (one lane): a ring of 128-byte-swizzled A / B tiles;
-//   warp 1     owner of the tensor memory and MMA issuer (one lane);
-//   warps 2-9  epilogue, two per tensor-memory lane quarter, half of the columns each.
-// Two accumulators let an item's epilogue overlap the next item's MMAs.
+// (output tile, K slice) with a static stride.  Warp roles (640 threads):
+//   warp 0      TMA producer (one lane): a ring of 128-byte-swizzled A / B tiles;
+//   warp 1      owner of the tensor memory and MMA issuer (one lane);
+//   warps 4-19  epilogue, four per tensor-memory lane quarter, a quarter of the columns each.
+// Two accumulators let an item's epilogue overlap the next item's MMAs.  The first four warps
+// hand registers to the epilogue (32 against 112 a thread, 96 at launch: 128 * 32 + 512 * 112
+// is 640 * 96).  With eight epilogue warps and 128 running sums a thread the epilogue, not the
+// MMAs, set the pace of products of few k-blocks.
 //
 // Tiles.  PAIR: 256 x BN per CTA pair (tcgen05.mma.cta_group::2); each CTA loads 128 rows
 // of A and half of B's BN.  BN = 256 streams 64 operand bytes per clock of tensor work, which
@@ -20,13 +23,21 @@
 // slices: each slice leaves its fp32 sums of the tile in the workspace, and a second kernel
 // joins them in slice order and runs the same epilogue.
 //
+// The backward pass's two products run as one launch: the items of the one with the longer K,
+// then the other's, so that neither's last wave leaves the GPU idle before the other starts.
+// The two single-thread roles branch once per item to code of its majors: with majors as run-time
+// values the MMA loop's descriptors left the uniform registers, and 8192 x 4096 -> 14336 took 711
+// instead of 627 us.
+//
 // Order.  Tiles run in bands of kBandRows tile rows, column by column inside a band, so the
 // tiles that are in flight together share few operand rows and columns in L2.
 //
-// Accuracy.  The tensor core's accumulation truncates: its error grows with every add.  16-bit
-// results accumulate the whole K (the error stays far below their rounding); an fp32 dW
-// accumulates kFoldBlocks * 64 of K in tensor memory at a time, and the epilogue adds
-// those sums in fp32 registers, rounded to nearest.
+// Accuracy.  The tensor core's accumulation truncates: its error grows with every add (a 4096
+// K of random terms: 2e-6 of the sum).  Results of 16 bits accumulate the whole K.  An fp32 dW,
+// and a forward product whose z is kept in 8 bits (where a sum's error decides which way a
+// value rounds), accumulate kFoldBlocks * 64 of K in tensor memory at a time, and the epilogue
+// adds those sums in fp32 registers, rounded to nearest: 1e-6, for 3 to 5 % of the time, the
+// tensor memory's reads.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -40,10 +51,12 @@ static __device__ DevStatus g_layer_status;
 constexpr int kBandRows = 8;
 constexpr int kFoldBlocks = 16;
 
+// Epilogues of the backward kernel; the forward kernel has its own (bias, activation,
+// residual, checkpoint of z).
 enum LinKind : int {
-  LIN_FORWARD = 0,  // bias, activation, residual, checkpoint of z
-  LIN_STORE = 1,    // out (16-bit) = acc
-  LIN_GRAD32 = 2,   // out (fp32) = acc, or += acc
+  LIN_STORE = 0,   // out (16-bit) = acc
+  LIN_GRAD32 = 1,  // out (fp32) = acc, or += acc
+  LIN_FORWARD = 2,
 };
 
 struct LinEpilogue {
@@ -54,21 +67,38 @@ struct LinEpilogue {
   CkptView k;
   long long ld_out, ld_res, ld_z;
   int M, N;
+  int kind;
   int act;
   int bias_f32;
   int accumulate;
 };
 
-struct LinParams {
+struct LinProblem {
   CUtensorMap mapA, mapB;
   LinEpilogue e;
-  float* part;  // [slice][tail tile][BM][BN]: sums of the sliced tiles
+  float* part;       // [slice][tail tile][BM][BN]: sums of the sliced tiles
+  int a_mn;          // A's major, 0: K, 1: MN (B: K in the forward kernel, MN in the backward one)
   int tiles_m, tiles_n;
   int full;          // tiles [0, full) are whole items, the tail's come as `slices` items each
   int slices;
   int items;
   int nk;            // k-blocks of 64
   int slice_blocks;  // k-blocks per slice
+  int fold;          // k-blocks per accumulation in tensor memory
+};
+
+// Partial column sums joined on the side by the epilogue warps, before their first tile:
+// out[c] = sum over p of part[p * cols + c].
+struct LinColSum {
+  const float* part;
+  float* out;  // nullptr: none
+  int parts, cols;
+};
+
+template <int NP>
+struct LinParams {
+  LinProblem p[NP];
+  LinColSum sum;
 };
 
 // ------------------------------------------------------------------ epilogue
@@ -99,11 +129,15 @@ __device__ __forceinline__ void store16x32(T* dst, const float* v, int n) {
 
 // The epilogue of 32 consecutive columns [col, col + 32) of one row; v holds the sums.
 // Columns come in eights (N is a multiple of 8).
-template <class T, int KIND>
+template <class T, bool FORWARD>
 __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int col, float* v) {
   if (row >= e.M || col >= e.N) return;
   const int n = min(32, e.N - col);
-  if constexpr (KIND == LIN_GRAD32) {
+  if constexpr (!FORWARD) {
+    if (e.kind == LIN_STORE) {
+      store16x32<T>(static_cast<T*>(e.out) + (long long)row * e.ld_out + col, v, n);
+      return;
+    }
     float* o = static_cast<float*>(e.out) + (long long)row * e.ld_out + col;
     if (e.accumulate) {
 #pragma unroll
@@ -120,8 +154,6 @@ __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int 
       for (int j = 0; j < 32; j += 4)
         if (j < n) *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     }
-  } else if constexpr (KIND == LIN_STORE) {
-    store16x32<T>(static_cast<T*>(e.out) + (long long)row * e.ld_out + col, v, n);
   } else {
     if (e.bias != nullptr) {
 #pragma unroll
@@ -193,9 +225,10 @@ struct LinCfg {
   static constexpr int STAGES = STAGE_BYTES > 24 * 1024 ? 6 : 8;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
   static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr int EPI_WARPS = 8;
-  static constexpr int COLS = BN / 2;  // columns per epilogue warp
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int EPI_WARPS = 16;
+  static constexpr int COLS = BN / 4;  // columns per epilogue warp
+  static constexpr int EPI_FIRST = 4;  // first epilogue warp
+  static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 };
 
 // Tile -> first row and column: bands of kBandRows tile rows, column by column.
@@ -208,6 +241,11 @@ __host__ __device__ __forceinline__ void lin_tile(int tile, int tiles_m, int til
   tm = first + r - tn * rows;
 }
 
+template <int N>
+struct IntC {
+  static constexpr int value = N;
+};
+
 struct LinItem {
   int m0, n0;    // first row / column of the tile
   int kb0, kb1;  // its k-blocks
@@ -215,7 +253,7 @@ struct LinItem {
 };
 
 template <class Cfg>
-__device__ __forceinline__ LinItem lin_item(const LinParams& p, int item) {
+__device__ __forceinline__ LinItem lin_item(const LinProblem& p, int item) {
   LinItem t;
   int tile = item, slice = 0;
   t.part = -1;
@@ -235,6 +273,10 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, int item) {
   return t;
 }
 
+// Inside each role's branch, so that the compiler knows which code has how many.
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 32;"); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); }
+
 // One operand's share of a stage: R rows (K-major) or R columns of 64 K rows (MN-major).
 template <bool PAIR, int MN_MAJOR, int R>
 __device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t bar_lead,
@@ -251,12 +293,12 @@ __device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* map, u
   }
 }
 
-template <class T, int KIND, int A_MN, int B_MN, bool PAIR, int BN>
-__device__ __forceinline__ void lin_body(const LinParams& p) {
+template <class T, bool FORWARD, bool PAIR, int BN>
+__device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& params) {
+  constexpr int NP = FORWARD ? 1 : 2;
   using Cfg = LinCfg<PAIR, BN>;
   constexpr int STAGES = Cfg::STAGES, BK = Cfg::BK;
-  constexpr uint32_t IDESC = make_idesc(Elem<T>::kDtype == MAO_BF16 ? 1u : 0u, A_MN, B_MN, Cfg::BM, Cfg::BN);
-  constexpr int FOLD = KIND == LIN_GRAD32 ? kFoldBlocks : (1 << 30);  // k-blocks per accumulation
+  constexpr int B_MN = FORWARD ? 0 : 1;
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];
@@ -304,8 +346,11 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
     }
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&p.mapA);
-    tma_prefetch_desc(&p.mapB);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      tma_prefetch_desc(&params.p[i].mapA);
+      tma_prefetch_desc(&params.p[i].mapB);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -313,14 +358,25 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
   volatile int* abort_flag = &abort_sh;
+  // item -> its problem: the second's items follow the first's
+  const int items = params.p[0].items + (NP > 1 ? params.p[NP - 1].items : 0);
+  auto problem = [&](int& item) -> const LinProblem& {
+    if (NP > 1 && item >= params.p[0].items) {
+      item -= params.p[0].items;
+      return params.p[NP - 1];
+    }
+    return params.p[0];
+  };
+  if constexpr (!FORWARD) wait_for_previous();  // the operands come from the kernel before
 
   if (warp == 0) {
+    give_registers();
     if (lane == 0) {
       // -------------------------------------------------------------- producer
       int it = 0;
       bool ok = true;
-      for (int item = worker; item < p.items && ok; item += workers) {
-        const LinItem t = lin_item<Cfg>(p, item);
+      auto load_item = [&](auto a_mn, const LinProblem& p, const LinItem& t) {
+        constexpr int A_MN = decltype(a_mn)::value;
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1;
@@ -340,18 +396,27 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
           lin_load<PAIR, B_MN, Cfg::BL>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK,
                                         t.n0 + Cfg::BL * (int)rank);
         }
+      };
+      for (int i = worker; i < items && ok; i += workers) {
+        int item = i;
+        const LinProblem& p = problem(item);
+        const LinItem t = lin_item<Cfg>(p, item);
+        if (!FORWARD && p.a_mn) load_item(IntC<1>{}, p, t);
+        else load_item(IntC<0>{}, p, t);
       }
       prod_it_sh = it;
     }
   } else if (warp == 1) {
+    give_registers();
     if (lane == 0 && leader) {
       // -------------------------------------------------------------- MMA issuer
       int it = 0, used = 0;
       bool ok = true;
-      for (int item = worker; item < p.items && ok; item += workers) {
-        const LinItem t = lin_item<Cfg>(p, item);
-        for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += FOLD) {
-          const int c1 = (t.kb1 - c0 > FOLD) ? c0 + FOLD : t.kb1;
+      auto mma_item = [&](auto a_mn, const LinItem& t, int fold) {
+        constexpr int A_MN = decltype(a_mn)::value;
+        constexpr uint32_t IDESC = make_idesc(Elem<T>::kDtype == MAO_BF16 ? 1u : 0u, A_MN, B_MN, Cfg::BM, Cfg::BN);
+        for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += fold) {
+          const int c1 = min(t.kb1, c0 + fold);
           const int acc = used & 1;
           const uint32_t aph = (used >> 1) & 1;
           ++used;
@@ -384,39 +449,71 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
           if constexpr (PAIR) umma_commit_pair(&tfull_bar[acc], 0x3);
           else umma_commit(&tfull_bar[acc]);
         }
+      };
+      for (int i = worker; i < items && ok; i += workers) {
+        int item = i;
+        const LinProblem& p = problem(item);
+        const LinItem t = lin_item<Cfg>(p, item);
+        if (!FORWARD && p.a_mn) mma_item(IntC<1>{}, t, p.fold);
+        else mma_item(IntC<0>{}, t, p.fold);
       }
       mma_it_sh = it;
       // every MMA issued here has finished before tensor memory is released
       if constexpr (PAIR) umma_commit_pair(&drain_bar, 0x3);
       else umma_commit(&drain_bar);
     }
+  } else if (warp < Cfg::EPI_FIRST) {
+    give_registers();
   } else {
+    take_registers();
     // ---------------------------------------------------------------- epilogue
     constexpr int COLS = Cfg::COLS;
     const int q = warp & 3;                   // tensor-memory lane quarter this warp may read
-    const int cb = ((warp - 2) >> 2) * COLS;  // its first column
+    const int cb = ((warp - Cfg::EPI_FIRST) >> 2) * COLS;  // its first column
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cb;
     uint32_t tempty_lead[2] = {0, 0};
     if constexpr (PAIR) {
       tempty_lead[0] = mapa_shared(smem_u32(&tempty_bar[0]), 0);
       tempty_lead[1] = mapa_shared(smem_u32(&tempty_bar[1]), 0);
     }
+    if constexpr (!FORWARD) {
+      // 32 columns at a time, the sixteen warps over the parts, joined in a fixed order
+      __shared__ float join[Cfg::EPI_WARPS][33];
+      const LinColSum& g = params.sum;
+      if (g.out != nullptr) {
+        for (int c0 = blockIdx.x * 32; c0 < g.cols; c0 += gridDim.x * 32) {
+          const int c = c0 + lane, w = warp - Cfg::EPI_FIRST;
+          float s = 0.0f;
+          if (c < g.cols) {
+            const float* src = g.part + c;
+            int i = w;
+            for (; i + 48 < g.parts; i += 64) {
+              const float v0 = src[(long long)i * g.cols], v1 = src[(long long)(i + 16) * g.cols],
+                          v2 = src[(long long)(i + 32) * g.cols], v3 = src[(long long)(i + 48) * g.cols];
+              s += (v0 + v1) + (v2 + v3);
+            }
+            for (; i < g.parts; i += 16) s += src[(long long)i * g.cols];
+          }
+          join[w][lane] = s;
+          asm volatile("bar.sync 1, 512;" ::: "memory");
+          if (w == 0 && c < g.cols) {
+#pragma unroll
+            for (int k = 1; k < Cfg::EPI_WARPS; ++k) s += join[k][lane];
+            g.out[c] = s;
+          }
+          asm volatile("bar.sync 1, 512;" ::: "memory");
+        }
+      }
+    }
     int used = 0;
     bool ok = true;
-    for (int item = worker; item < p.items && ok; item += workers) {
+    for (int i = worker; i < items && ok; i += workers) {
+      int item = i;
+      const LinProblem& p = problem(item);
       const LinItem t = lin_item<Cfg>(p, item);
       const int row = t.m0 + 128 * (int)rank + q * 32 + lane;
-      const int col = t.n0 + cb;
-      // what a 32-column chunk becomes: sums of a K slice, or the result.  All of a sliced
-      // tile is stored, rows and columns behind the matrix too: they are zeros
-      auto finish = [&](int ch, float* v) {
-        if (t.part >= 0) {
-          store_f32x32(p.part + ((long long)t.part * Cfg::BM + (row - t.m0)) * Cfg::BN + cb + ch * 32, v);
-        } else {
-          lin_epilogue<T, KIND>(p.e, row, col + ch * 32, v);
-        }
-      };
-      if constexpr (KIND != LIN_GRAD32) {
+      float run[COLS];
+      for (int c0 = t.kb0; c0 < t.kb1; c0 += p.fold) {
         const int acc = used & 1;
         const bool w = mbar_wait(&tfull_bar[acc], (used >> 1) & 1, status, 54, abort_flag);
         ++used;
@@ -425,47 +522,36 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
           break;
         }
         tc_fence_after();
-#pragma unroll 1
+        const bool first = c0 == t.kb0;
+#pragma unroll
         for (int ch = 0; ch < COLS / 32; ++ch) {
           uint32_t rr[32];
           tmem_ld_32x32b_x32(lane_base + acc * Cfg::BN + ch * 32, rr);
           tmem_wait_ld();
-          float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(rr[j]);
-          finish(ch, v);
+          for (int j = 0; j < 32; ++j)
+            run[ch * 32 + j] = first ? __uint_as_float(rr[j]) : run[ch * 32 + j] + __uint_as_float(rr[j]);
         }
         tc_fence_before();
         if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty_lead[acc]);
         else mbar_arrive_relaxed(&tempty_bar[acc]);
-      } else {
-        float run[COLS];
+      }
+      if (!ok) break;
+      // The chunks of 32 columns through one copy of the epilogue's code (unrolled, it would
+      // be fetched anew for every chunk of a short product): the sums move down by a chunk.
+#pragma unroll 1
+      for (int ch = 0; ch < COLS / 32; ++ch) {
+        float v[32];
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) run[j] = 0.0f;
-        for (int c0 = t.kb0; c0 < t.kb1; c0 += FOLD) {
-          const int acc = used & 1;
-          const bool w = mbar_wait(&tfull_bar[acc], (used >> 1) & 1, status, 54, abort_flag);
-          ++used;
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        for (int j = 0; j < 32; ++j) v[j] = run[j];
 #pragma unroll
-          for (int ch = 0; ch < COLS / 32; ++ch) {
-            uint32_t rr[32];
-            tmem_ld_32x32b_x32(lane_base + acc * Cfg::BN + ch * 32, rr);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) run[ch * 32 + j] += __uint_as_float(rr[j]);
-          }
-          tc_fence_before();
-          if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty_lead[acc]);
-          else mbar_arrive_relaxed(&tempty_bar[acc]);
+        for (int j = 0; j + 32 < COLS; ++j) run[j] = run[j + 32];
+        if (t.part >= 0) {
+          // all of a sliced tile is stored, what lies behind the matrix too: zeros
+          store_f32x32(p.part + ((long long)t.part * Cfg::BM + (row - t.m0)) * Cfg::BN + cb + ch * 32, v);
+        } else {
+          lin_epilogue<T, FORWARD>(p.e, row, t.n0 + cb + ch * 32, v);
         }
-        if (!ok) break;
-#pragma unroll
-        for (int ch = 0; ch < COLS / 32; ++ch) finish(ch, &run[ch * 32]);
       }
     }
   }
@@ -492,28 +578,38 @@ __device__ __forceinline__ void lin_body(const LinParams& p) {
   }
 }
 
-template <class T, int KIND, int A_MN, int B_MN, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
-    lin_pair_kernel(const __grid_constant__ LinParams p) {
-  lin_body<T, KIND, A_MN, B_MN, true, BN>(p);
+template <class T, bool FORWARD, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(640, 1)
+    lin_pair_kernel(const __grid_constant__ LinParams<FORWARD ? 1 : 2> p) {
+  lin_body<T, FORWARD, true, BN>(p);
 }
 
-template <class T, int KIND, int A_MN, int B_MN>
-__global__ void __launch_bounds__(320, 1) lin_kernel(const __grid_constant__ LinParams p) {
-  lin_body<T, KIND, A_MN, B_MN, false, 128>(p);
+template <class T, bool FORWARD>
+__global__ void __launch_bounds__(640, 1) lin_kernel(const __grid_constant__ LinParams<FORWARD ? 1 : 2> p) {
+  lin_body<T, FORWARD, false, 128>(p);
 }
 
-// Joins the slices of the tail's tiles in slice order and runs the epilogue.  A thread owns
-// 32 columns of a row, as in the product kernel.
+// Joins the slices of the tails' tiles in slice order and runs the epilogue.  A thread owns
+// 32 columns of a row, as in the product kernel.  pieces: 32-column pieces of the first
+// problem's tail; the second's follow.
 struct LinJoin {
   LinEpilogue e;
   const float* part;
   int tiles_m, tiles_n, full, slices;
 };
-template <class T, int KIND, int BM, int BN>
-__global__ void __launch_bounds__(128) lin_join_kernel(const LinJoin p) {
+template <int NP>
+struct LinJoins {
+  LinJoin p[NP];
+  int pieces;
+};
+template <class T, bool FORWARD, int BM, int BN>
+__global__ void __launch_bounds__(128) lin_join_kernel(const LinJoins<FORWARD ? 1 : 2> a) {
+  wait_for_previous();
+  int i = blockIdx.x * 128 + threadIdx.x;
+  const bool second = !FORWARD && i >= a.pieces;  // the same for a block: pieces is a multiple of 128
+  if (second) i -= a.pieces;
+  const LinJoin& p = a.p[second ? 1 : 0];
   const int tail = p.tiles_m * p.tiles_n - p.full;
-  const int i = blockIdx.x * 128 + threadIdx.x;  // 32-column pieces of the tail's tiles
   const int tile = i / (BM * BN / 32);
   const int r = i - tile * (BM * BN / 32);
   int tm, tn;
@@ -527,11 +623,11 @@ __global__ void __launch_bounds__(128) lin_join_kernel(const LinJoin p) {
   for (int k = 0; k < p.slices; ++k, s += (long long)tail * BM * BN) {
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(s + j));
-      v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w;
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(s + j));
+      v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
     }
   }
-  lin_epilogue<T, KIND>(p.e, row, col, v);
+  lin_epilogue<T, FORWARD>(p.e, row, col, v);
 }
 
 }  // namespace mao

@@ -315,15 +315,24 @@ def test_linear_backward(api, rows, n, m, dt):
 
 
 def test_linear_backward_parts(api):
-    """Each output alone has the bits it has among the others."""
+    """Each output alone is what it is among the others.  The products of a call share a launch,
+    and how K is cut depends on all of them, so sums may be joined in another order: each of the
+    two results is off by at most (K / 16 + 20) truncated adds of the sum of magnitudes (db: its
+    chain of adds), and dx is rounded to bf16 after that, which may move it by a step."""
     g = _gen(2)
     x, w = _randn(g, 200, 256, dtype=torch.bfloat16), _randn(g, 512, 256, std=0.06, dtype=torch.bfloat16)
     dy, z = _randn(g, 200, 512, dtype=torch.bfloat16), _randn(g, 200, 512, dtype=torch.bfloat16)
     dx, dw, db = api.linear_backward(dy, x, w, z=z, act="silu")
+    dz = (dy.double() * R.slope(z.double(), "silu")).abs() * (1 + R.HALF_STEP[torch.bfloat16])
+    tol = (2 * (512 / 16 + 20) * R.TC * (dz @ w.double().abs()) + 2 * 1.01 * R.HALF_STEP[torch.bfloat16] * dx.double().abs(),
+           2 * (200 / 16 + 20) * R.TC * (dz.t() @ x.double().abs()), 2 * 216 * R.F32 * dz.sum(0))
     for need in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 0, 0)):
         got = api.linear_backward(dy, x, w, z=z, act="silu", need_dx=need[0], need_dw=need[1], need_db=need[2])
-        for a, b, n in zip(got, (dx, dw, db), need):
-            assert (a is None) if not n else torch.equal(a, b)
+        for a, b, n, t in zip(got, (dx, dw, db), need, tol):
+            if n:
+                R.close(a, b, t, "alone")
+            else:
+                assert a is None
 
 
 def test_linear_empty(api):
