@@ -16,93 +16,116 @@ struct Shape {
 };
 struct LinPlan {
   int tiles_m = 0, tiles_n = 0, nk = 0, full = 0, slices = 1, slice_blocks = 0;
-  int items = 0;
   size_t part_bytes = 0;
+  int items() const { return full + (tiles_m * tiles_n - full) * slices; }
 };
 struct LinPlans {
   int tile = TILE_ONE;
-  LinPlan p[2];
+  LinPlan p[2];  // one product: p[0]
+  LinDeal deal = {};
   size_t part_bytes() const { return p[0].part_bytes + p[1].part_bytes; }
 };
 
-// Tiles and K slices of one product, or of two that share a launch (the longer K first), from
-// their sizes alone (and so the same on every device and in the workspace query): the
-// cheapest by estimated nanoseconds.
-bool plan_of(const Shape* q, int n, LinPlans* out) {
-  // a k-block of 64; set-up, first loads and last epilogue; the joining kernel
+// Sets a plan to `whole` unsliced tiles and the others in s slices; false if that makes none.
+bool cut(LinPlan& p, int whole, int s, int tile_bytes) {
+  p.full = whole;
+  p.slices = s;
+  p.slice_blocks = (p.nk + s - 1) / s;
+  const long long rest = (long long)p.tiles_m * p.tiles_n - whole;
+  p.part_bytes = s > 1 ? (size_t)s * (size_t)rest * tile_bytes : 0;
+  return s == 1 || (rest > 0 && p.slice_blocks >= 4 && (p.nk + p.slice_blocks - 1) / p.slice_blocks == s);
+}
+
+// Tiles, K slices and the dealing of one product, or of two that share a launch (the longer K
+// first), from their sizes alone (and so the same on every device and in the workspace
+// query): of the candidates, the one whose longest list is estimated to end first.
+bool search_plan(const Shape* q, int n, LinPlans* out) {
+  // ns, measured: a k-block of 64; set-up, first loads and last epilogue; the joining kernel
   constexpr double kBlock[3] = {385.0, 300.0, 320.0}, kFixed[3] = {6500.0, 5500.0, 5000.0};
   constexpr double kJoin = 3500.0, kJoinBytes = 4000.0;  // its launch; bytes per ns, written and read
+  constexpr int kSlices[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   double best = 1e300;
   for (int t = 0; t < 3; ++t) {
-    const long long workers = t == TILE_ONE ? kPlanSms : kPlanSms / 2;
+    const long long W = t == TILE_ONE ? kPlanSms : kPlanSms / 2;
+    const int tile_bytes = 4 * kTileM[t] * kTileN[t];
     LinPlans c;
     c.tile = t;
-    long long tiles[2] = {0, 0};
     bool fits = true;
     for (int i = 0; i < n; ++i) {
       const long long tm = (q[i].M + kTileM[t] - 1) / kTileM[t], tn = (q[i].N + kTileN[t] - 1) / kTileN[t];
-      tiles[i] = tm * tn;
-      fits = fits && tiles[i] <= (1ll << 27);
+      fits = fits && tm * tn <= (1ll << 26);
       c.p[i].tiles_m = (int)tm, c.p[i].tiles_n = (int)tn;
       c.p[i].nk = (int)((q[i].K + 63) / 64);
     }
     if (!fits) continue;
-    // cut[i]: tiles of problem i behind the last full wave of the launch; slices for each
-    const long long rest = (tiles[0] + tiles[1]) % workers;
-    const long long cut[2] = {n == 1 ? rest : std::max(0ll, rest - tiles[1]), n == 1 ? 0 : std::min(rest, tiles[1])};
-    for (int s0 = 1; s0 <= 16; ++s0) {
-      for (int s1 = 1; s1 <= 16; ++s1) {
-        const int s[2] = {s0, s1};
-        // whole items of every problem, then the slices, dealt in turn to the workers: the
-        // length of the longest is estimated by the mean plus the longest item
-        double sum = 0.0, longest = 0.0, bytes = 0.0;
-        bool ok = true;
-        for (int i = 0; i < 2; ++i) {
-          LinPlan& p = c.p[i];
-          const bool sliced = s[i] > 1;
-          if (i >= n || cut[i] == 0 || p.nk < 8) {
-            if (sliced) ok = false;
-            if (i >= n) continue;
+    LinPlan& last = c.p[n - 1];
+    const long long tiles0 = n > 1 ? (long long)c.p[0].tiles_m * c.p[0].tiles_n : 0;
+    const long long tiles1 = (long long)last.tiles_m * last.tiles_n;
+    for (int s0 : kSlices) {
+      if (s0 > 1 && (n == 1 || tiles0 >= W)) break;  // the first is cut as a whole, where it is small
+      if (n > 1 && !cut(c.p[0], s0 > 1 ? 0 : (int)tiles0, s0, tile_bytes)) continue;
+      const long long first = tiles0 * s0, len0 = n > 1 ? c.p[0].slice_blocks : 0;
+      const long long extra = first % W, others = W - extra, base = first / W * len0;
+      const long long len1 = last.nk;
+      // whole items of the last problem per list, so that the lists end about together
+      const long long total = first * len0 + tiles1 * len1;
+      const long long y0 = std::max(0ll, (total / W - base) / len1), x0 = std::max(0ll, (total / W - base - len0) / len1);
+      for (long long y = y0; y >= std::max(0ll, y0 - 1); --y) {
+        for (long long x = extra > 0 ? x0 : 0; x >= std::max(0ll, x0 - 1) || x == 0; --x) {
+          if (x > y) continue;
+          const long long whole = std::min(tiles1, others * y + extra * x);
+          const long long rest = tiles1 - whole;
+          for (int s1 : kSlices) {
+            if (s1 > 1 && rest == 0) break;
+            if (!cut(last, s1 > 1 ? (int)whole : (int)tiles1, s1, tile_bytes)) continue;
+            const long long cuts = rest * s1, len = last.slice_blocks;
+            const long long most = (cuts + others - 1) / others;
+            for (long long v = extra > 0 ? 0 : most; v <= std::min(most, 40ll) || extra == 0; ++v) {
+              const long long u = extra > 0 ? (std::max(0ll, cuts - others * v) + extra - 1) / extra : 0;
+              const long long longest = base + std::max(y * len1 + v * len, extra > 0 ? len0 + x * len1 + u * len : 0ll);
+              const size_t bytes = c.part_bytes();
+              const double cost = (double)longest * kBlock[t] + kFixed[t] +
+                                  (bytes > 0 ? kJoin + 2.0 * (double)bytes / kJoinBytes : 0.0);
+              if (cost < best) {
+                best = cost;
+                c.deal = LinDeal{(int)W, (int)first, (int)extra, (int)whole, (int)y, (int)(extra > 0 ? y - x : 0), (int)cuts, (int)v};
+                *out = c;
+              }
+              if (extra == 0) break;
+            }
           }
-          p.slices = s[i];
-          p.slice_blocks = (p.nk + s[i] - 1) / s[i];
-          if (sliced && (p.slice_blocks < 4 || (p.nk + p.slice_blocks - 1) / p.slice_blocks != s[i])) ok = false;
-          if (!ok) break;
-          p.full = (int)(sliced ? tiles[i] - cut[i] : tiles[i]);
-          p.items = p.full + (int)(tiles[i] - p.full) * p.slices;
-          p.part_bytes = sliced ? 4ull * p.slices * (size_t)cut[i] * kTileM[t] * kTileN[t] : 0;
-          sum += (double)tiles[i] * p.nk;
-          bytes += (double)p.part_bytes;
-        }
-        if (!ok) continue;
-        // deal the items out: worker w gets items w, w + workers, ...
-        const long long n0 = c.p[0].items, n1 = n > 1 ? c.p[1].items : 0, all = n0 + n1;
-        const long long per = all / workers, left = all - per * workers;
-        auto len = [&](long long item) -> double {
-          const LinPlan& p = item < n0 ? c.p[0] : c.p[1];
-          const long long k = item < n0 ? item : item - n0;
-          return k < p.full ? p.nk : p.slice_blocks;
-        };
-        // the first, last and boundary workers hold the extremes
-        const long long probe[4] = {0, left > 0 ? left - 1 : workers - 1, n0 % workers, (c.p[0].full) % workers};
-        for (long long w : probe) {
-          double l = 0.0;
-          if (all <= 64 * workers) {
-            for (long long i = w; i < all; i += workers) l += len(i);
-          } else {
-            l = (double)(sum / workers) + len(all - 1);
-          }
-          longest = std::max(longest, l);
-        }
-        const double cost = longest * kBlock[t] + kFixed[t] + (bytes > 0 ? kJoin + 2.0 * bytes / kJoinBytes : 0.0);
-        if (cost < best) {
-          best = cost;
-          *out = c;
+          if (x == 0) break;
         }
       }
     }
   }
   return best < 1e300;
+}
+
+// The search takes some tens of microseconds; a program calls with few sizes, so each thread
+// keeps the plans of its latest ones.
+bool plan_of(const Shape* q, int n, LinPlans* out) {
+  struct Entry {
+    int n = 0;
+    Shape q[2] = {};
+    LinPlans plans;
+  };
+  static thread_local Entry cache[32];
+  unsigned long long h = (unsigned long long)n;
+  for (int i = 0; i < n; ++i)
+    h = (((h * 0x9E3779B97F4A7C15ull + (unsigned long long)q[i].M) * 0x9E3779B97F4A7C15ull + (unsigned long long)q[i].N) *
+         0x9E3779B97F4A7C15ull) + (unsigned long long)q[i].K;
+  Entry& e = cache[(h * 0x9E3779B97F4A7C15ull) >> 59];
+  bool same = e.n == n;
+  for (int i = 0; same && i < n; ++i) same = e.q[i].M == q[i].M && e.q[i].N == q[i].N && e.q[i].K == q[i].K;
+  if (!same) {
+    e.n = 0;
+    if (!search_plan(q, n, &e.plans)) return false;
+    for (int i = 0; i < n; ++i) e.q[i] = q[i];
+    e.n = n;
+  }
+  *out = e.plans;
+  return true;
 }
 
 // ------------------------------------------------------------------ launch
@@ -115,7 +138,7 @@ mao_status launch_product(const LinParams<FORWARD ? 1 : 2>& p, int items, bool d
   else kern = lin_kernel<T, FORWARD>;
   static std::atomic<bool> done[64];
   MAO_TRY(allow_smem(kern, Cfg::SMEM_BYTES, done));
-  const int workers = std::min(items, PAIR ? dev.sm_count / 2 : dev.sm_count);
+  const int workers = std::min({items, p.deal.workers, PAIR ? dev.sm_count / 2 : dev.sm_count});
   const int grid = PAIR ? 2 * workers : workers;
   if (dependent) return launch_dependent(kern, dim3(grid), Cfg::THREADS, Cfg::SMEM_BYTES, stream, p);
   kern<<<grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(p);
@@ -155,11 +178,13 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
   std::memset(&a, 0, sizeof(a));
   std::memset(&j, 0, sizeof(j));
   a.sum = sum;
+  a.deal = plans.deal;
   double flops = 0.0;
   int items = 0, pieces = 0;
   for (int i = 0; i < n; ++i) {
     const LinPlan& c = plans.p[i];
-    LinProblem& p = a.p[i];
+    const int slot = i + NP - n;  // a single product of the backward pass is its kernel's last
+    LinProblem& p = a.p[slot];
     MAO_TRY(encode(&p.mapA, Elem<T>::kDtype, q[i].A, q[i].a_mn, 128));
     MAO_TRY(encode(&p.mapB, Elem<T>::kDtype, q[i].B, !FORWARD, plans.tile == TILE_PAIR128 ? 64 : 128));
     p.e = q[i].e;
@@ -167,23 +192,21 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
     part += c.part_bytes / sizeof(float);
     p.a_mn = q[i].a_mn;
     p.tiles_m = c.tiles_m, p.tiles_n = c.tiles_n;
-    p.full = c.full, p.slices = c.slices, p.items = c.items;
+    p.full = c.full, p.slices = c.slices;
     p.nk = c.nk, p.slice_blocks = c.slice_blocks;
     p.fold = p.e.kind == LIN_GRAD32 || p.e.k.q != nullptr ? kFoldBlocks : p.nk;
-    items += c.items;
+    items += c.items();
     const Shape s = q[i].shape();
     flops += 2.0 * (double)s.M * (double)s.N * (double)s.K;
-    j.p[i] = LinJoin{p.e, p.part, c.tiles_m, c.tiles_n, c.full, c.slices};
+    j.p[slot] = LinJoin{p.e, p.part, c.tiles_m, c.tiles_n, c.full, c.slices};
     if (c.slices > 1) {
-      // at most one wave of tiles: far below 2^31 pieces, a multiple of 128
+      // a few rounds of tiles at most: far below 2^31 pieces, a multiple of 128
       const int k = (c.tiles_m * c.tiles_n - c.full) * (kTileM[plans.tile] * kTileN[plans.tile] / 32);
-      if (i == 0) j.pieces = k;
+      if (slot == 0) j.pieces = k;
       pieces += k;
     }
   }
-  for (int i = n; i < NP; ++i) {  // an absent second problem has no items; its maps are only prefetched
-    a.p[i].mapA = a.p[0].mapA, a.p[i].mapB = a.p[0].mapB;
-  }
+  if (n < NP) a.p[0].mapA = a.p[NP - 1].mapA, a.p[0].mapB = a.p[NP - 1].mapB;  // prefetched, not used
   {
     LaunchScope ls(stream, kernel_id, flops, bytes);
     switch (plans.tile) {

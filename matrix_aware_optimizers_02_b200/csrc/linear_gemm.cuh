@@ -5,8 +5,8 @@
 //   dx         dx = dz W                   A = dz (K-major),     B = W (MN-major)
 //   dW         dW = dz^T x                 A = dz (MN-major),    B = x (MN-major)
 //
-// One persistent kernel, one CTA per SM or one CTA pair per two SMs, walking work items
-// (output tile, K slice) with a static stride.  Warp roles (640 threads):
+// One persistent kernel, one CTA per SM or one CTA pair per two SMs, each walking a list of work
+// items (output tile, K slice) that the host's plan dealt it.  Warp roles (640 threads):
 //   warp 0      TMA producer (one lane): a ring of 128-byte-swizzled A / B tiles;
 //   warp 1      owner of the tensor memory and MMA issuer (one lane);
 //   warps 4-19  epilogue, four per tensor-memory lane quarter, a quarter of the columns each.
@@ -19,12 +19,12 @@
 // of A and half of B's BN.  BN = 256 streams 64 operand bytes per clock of tensor work, which
 // leaves shared memory room to refill; BN = 128 is for products whose 256 x 256 tiles leave
 // SMs idle.  One CTA: 128 x 128, for products of up to 128 rows.
-// The tiles behind the last full wave (all of them, where there are few) may be cut into K
-// slices: each slice leaves its fp32 sums of the tile in the workspace, and a second kernel
-// joins them in slice order and runs the same epilogue.
+// Tiles that do not fill a whole round of the workers may be cut into K slices: each slice
+// leaves its fp32 sums of the tile in the workspace, and a second kernel joins them in slice
+// order and runs the same epilogue.
 //
-// The backward pass's two products run as one launch: the items of the one with the longer K,
-// then the other's, so that neither's last wave leaves the GPU idle before the other starts.
+// The backward pass's two products run as one launch, the one with the longer K first, dealt
+// so that the workers left over by its last round take more of the other (LinDeal).
 // The two single-thread roles branch once per item to code of its majors: with majors as run-time
 // values the MMA loop's descriptors left the uniform registers, and 8192 x 4096 -> 14336 took 711
 // instead of 627 us.
@@ -76,12 +76,11 @@ struct LinEpilogue {
 struct LinProblem {
   CUtensorMap mapA, mapB;
   LinEpilogue e;
-  float* part;       // [slice][tail tile][BM][BN]: sums of the sliced tiles
+  float* part;       // [slice][sliced tile][BM][BN]: sums of the sliced tiles
   int a_mn;          // A's major, 0: K, 1: MN (B: K in the forward kernel, MN in the backward one)
   int tiles_m, tiles_n;
-  int full;          // tiles [0, full) are whole items, the tail's come as `slices` items each
+  int full;          // tiles [0, full) are whole items, the others come as `slices` items each
   int slices;
-  int items;
   int nk;            // k-blocks of 64
   int slice_blocks;  // k-blocks per slice
   int fold;          // k-blocks per accumulation in tensor memory
@@ -95,10 +94,65 @@ struct LinColSum {
   int parts, cols;
 };
 
+// Which worker does what.  List w has the first problem's items w, w + workers, ...; `extra`
+// lists have one more of those than the others.  Of the last problem's `whole` items the other
+// lists take `lead` each in turn, then all lists take theirs in turn (so that what runs at one
+// time lies together in L2), `per_whole` in all for the others.  Its `cuts` items behind those
+// (slices, or single tiles) go in turn to the others, at most `per_cut` each, and what is left
+// in turn to the lists with an extra.
+struct LinDeal {
+  int workers;
+  int first;  // items of the first of two problems, 0 where there is one
+  int extra;
+  int whole, per_whole, lead;
+  int cuts, per_cut;
+};
+
 template <int NP>
 struct LinParams {
   LinProblem p[NP];
+  LinDeal deal;
   LinColSum sum;
+};
+
+template <int NP>
+struct LinWalk {
+  int w, step, phase, k;
+  __host__ __device__ __forceinline__ LinWalk(int worker, int workers) : w(worker), step(workers), phase(NP > 1 ? 0 : 1), k(0) {}
+  // the next item of this worker's lists; false: none left
+  __host__ __device__ __forceinline__ bool next(const LinDeal& d, int& problem, int& item) {
+    for (; w < d.workers; w += step, phase = (NP > 1 ? 0 : 1), k = 0) {
+      if (NP > 1 && phase == 0) {
+        item = w + k * d.workers;
+        if (item < d.first) {
+          ++k;
+          problem = 0;
+          return true;
+        }
+        phase = 1, k = 0;
+      }
+      const int others = d.workers - d.extra;
+      const bool plain = w >= d.extra;
+      if (phase == 1) {
+        const int late = plain ? k - d.lead : k;  // rounds of all lists behind it
+        item = late < 0 ? w - d.extra + k * others : others * d.lead + late * d.workers + w;
+        if (item < d.whole && k < (plain ? d.per_whole : d.per_whole - d.lead)) {
+          ++k;
+          problem = NP - 1;
+          return true;
+        }
+        phase = 2, k = 0;
+      }
+      item = plain ? w - d.extra + k * others : others * d.per_cut + w + k * d.extra;
+      if (item < d.cuts && (!plain || k < d.per_cut)) {
+        ++k;
+        problem = NP - 1;
+        item += d.whole;
+        return true;
+      }
+    }
+    return false;
+  }
 };
 
 // ------------------------------------------------------------------ epilogue
@@ -358,15 +412,6 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
   volatile int* abort_flag = &abort_sh;
-  // item -> its problem: the second's items follow the first's
-  const int items = params.p[0].items + (NP > 1 ? params.p[NP - 1].items : 0);
-  auto problem = [&](int& item) -> const LinProblem& {
-    if (NP > 1 && item >= params.p[0].items) {
-      item -= params.p[0].items;
-      return params.p[NP - 1];
-    }
-    return params.p[0];
-  };
   if constexpr (!FORWARD) wait_for_previous();  // the operands come from the kernel before
 
   if (warp == 0) {
@@ -397,9 +442,9 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
                                         t.n0 + Cfg::BL * (int)rank);
         }
       };
-      for (int i = worker; i < items && ok; i += workers) {
-        int item = i;
-        const LinProblem& p = problem(item);
+      LinWalk<NP> walk(worker, workers);
+      for (int which = 0, item = 0; ok && walk.next(params.deal, which, item);) {
+        const LinProblem& p = params.p[which];
         const LinItem t = lin_item<Cfg>(p, item);
         if (!FORWARD && p.a_mn) load_item(IntC<1>{}, p, t);
         else load_item(IntC<0>{}, p, t);
@@ -450,9 +495,9 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
           else umma_commit(&tfull_bar[acc]);
         }
       };
-      for (int i = worker; i < items && ok; i += workers) {
-        int item = i;
-        const LinProblem& p = problem(item);
+      LinWalk<NP> walk(worker, workers);
+      for (int which = 0, item = 0; ok && walk.next(params.deal, which, item);) {
+        const LinProblem& p = params.p[which];
         const LinItem t = lin_item<Cfg>(p, item);
         if (!FORWARD && p.a_mn) mma_item(IntC<1>{}, t, p.fold);
         else mma_item(IntC<0>{}, t, p.fold);
@@ -507,9 +552,9 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
     }
     int used = 0;
     bool ok = true;
-    for (int i = worker; i < items && ok; i += workers) {
-      int item = i;
-      const LinProblem& p = problem(item);
+    LinWalk<NP> walk(worker, workers);
+    for (int which = 0, item = 0; ok && walk.next(params.deal, which, item);) {
+      const LinProblem& p = params.p[which];
       const LinItem t = lin_item<Cfg>(p, item);
       const int row = t.m0 + 128 * (int)rank + q * 32 + lane;
       float run[COLS];
