@@ -197,11 +197,14 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 // A thread's own ring in shared memory: cp.async of 16 (or 8) bytes that only the issuing
 // thread reads back, so no barrier orders them, only its own wait.  With ok false nothing is
 // read and zeros are written.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok = true) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok = true) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void sts_zero8(uint32_t dst) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the latest N groups of this thread have landed
@@ -228,9 +231,13 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
 template <class T>
 struct Slot8 {
   static constexpr int kBytes = 8 * sizeof(T);
-  static __device__ __forceinline__ void fetch(uint32_t dst, uint32_t stride, const T* src, bool ok) {
+  static __device__ __forceinline__ void fetch(uint32_t dst, uint32_t stride, const T* src) {
 #pragma unroll
-    for (int i = 0; i < kBytes / 16; ++i) cp_async16(dst + i * stride, src + i * (16 / sizeof(T)), ok);
+    for (int i = 0; i < kBytes / 16; ++i) cp_async16(dst + i * stride, src + i * (16 / sizeof(T)));
+  }
+  static __device__ __forceinline__ void zero(uint32_t dst, uint32_t stride) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 16; ++i) sts_zero8(dst + i * stride), sts_zero8(dst + i * stride + 8);
   }
   static __device__ __forceinline__ Vec8<T> get(uint32_t src, uint32_t stride) {
     Vec8<T> t;

@@ -21,24 +21,39 @@ namespace {
 // call is enough: a buffer is written again only after the barrier of the call between.
 template <int G, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* sh) {
+  const bool low = (threadIdx.x & 16) == 0;
+  float s = v[0];
+  if constexpr (N == 2) {
+    // lanes 0-15 go on with the first sum, lanes 16-31 with the second
+    const float mine = low ? v[0] : v[1], other = low ? v[1] : v[0];
+    s = mine + __shfl_xor_sync(0xffffffffu, other, 16);
+  } else {
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if constexpr (G > 32) {
     constexpr int W = G / 32;  // warps of a row
     const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) sh[warp * N + i] = v[i];
-    }
+    if ((threadIdx.x & (N == 2 ? 15 : 31)) == 0) sh[warp * N + (low ? 0 : 1)] = s;
     __syncthreads();
-    const float2* r = reinterpret_cast<const float2*>(sh + (warp / W) * W * N);
+    const float* r = sh + (warp / W) * W * N;
     f2 p = dup2(0.0f);  // N = 1: even and odd warps; N = 2: the two sums
+    if constexpr (W * N >= 4) {
 #pragma unroll
-    for (int w = 0; w < W * N / 2; ++w) p = add2(p, r[w]);
+      for (int w = 0; w < W * N / 4; ++w) {
+        const float4 q = reinterpret_cast<const float4*>(r)[w];
+        p = add2(p, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+      }
+    } else {
+      p = *reinterpret_cast<const float2*>(r);
+    }
     if constexpr (N == 1) v[0] = p.x + p.y;
     else v[0] = p.x, v[1] = p.y;
+  } else if constexpr (N == 1) {
+    v[0] = s;
+  } else {
+    v[0] = __shfl_sync(0xffffffffu, s, 0), v[1] = __shfl_sync(0xffffffffu, s, 16);
   }
 }
 
@@ -55,11 +70,13 @@ constexpr int ring_stages(int bytes_per_thread, int resident) {
   return n > kMostStages ? kMostStages : n;
 }
 
+// Row indices are unsigned: a row ahead of the last one does not overflow.
 template <class T>
-__device__ __forceinline__ void load_vec(const T* p, long long ld, long long row, int c, int rows, int cols,
-                                         Vec8<T>& x) {
-  if (row < rows && c < cols) x.load(p + row * ld + c);
+__device__ __forceinline__ Vec8<T> load_vec(const T* p, bool ok) {
+  Vec8<T> x;
+  if (ok) x.load(p);
   else x.zero();
+  return x;
 }
 
 // ------------------------------------------------------------------ forward
@@ -97,21 +114,36 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
   const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
   const int t = threadIdx.x % G;
   const int cols = a.cols;
-  const T* x = static_cast<const T*>(a.x);
-  const long long step = (long long)gridDim.x * R;
-  const long long row0 = (long long)blockIdx.x * R + threadIdx.x / G;
-  auto fetch = [&](long long r, int stage) {
-    if constexpr (D == 0) return;
+  const uint32_t step = gridDim.x * R, rows = (uint32_t)a.rows;
+  const uint32_t row0 = blockIdx.x * R + threadIdx.x / G;
+  bool in[VPT];  // vectors inside the row
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * G + t) * 8;
-      const bool ok = r < a.rows && c < cols;
-      Slot8<T>::fetch(slot0 + (stage * VPT + i) * kVec, B * 16, ok ? x + r * a.ld_x + c : x, ok);
+  for (int i = 0; i < VPT; ++i) in[i] = (i * G + t) * 8 < cols;
+  // where the row ahead and the present row's results lie, moved on by a step per row
+  const T* ahead = static_cast<const T*>(a.x) + (long long)row0 * a.ld_x + t * 8;
+  const long long ahead_step = (long long)step * a.ld_x, y_step = (long long)step * a.ld_y;
+  T* y = static_cast<T*>(a.y) + (long long)row0 * a.ld_y + t * 8;
+  uint32_t row_ahead = row0;
+  auto fetch = [&](int stage) {
+    if (row_ahead < rows) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (in[i]) Slot8<T>::fetch(slot0 + (stage * VPT + i) * kVec, B * 16, ahead + i * G * 8);
     }
     cp_async_commit();
+    row_ahead += step;
+    ahead += ahead_step;
   };
+  if constexpr (D > 0) {
+    // slots behind the last column hold zeros for good
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) fetch(row0 + d * step, d);
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (!in[i]) Slot8<T>::zero(slot0 + (d * VPT + i) * kVec, B * 16);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) fetch(d);
+  }
   f2 w[VPT][4], b[VPT][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -123,22 +155,25 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
       if (a.b != nullptr) load_param8<T>(a.b, a.w_f32, c, b[i]);
     }
   }
-  long long row = row0;
+  uint32_t row = row0;
   int stage = 0;
-  // the trip count is the block's: rows behind the last take part in the reductions
-  for (long long r0 = (long long)blockIdx.x * R; r0 < a.rows; r0 += step, row += step) {
-    // the slot read in the iteration before is free: its values are in registers and used
-    fetch(row + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
-    if constexpr (D > 0) cp_async_wait<D - 1>();
+  // the trip count is the block's: rows behind the last take part in the reductions, with
+  // whatever their slots hold, and write nothing
+  for (uint32_t r0 = blockIdx.x * R; r0 < rows; r0 += step, row += step, y += y_step) {
+    const bool live = row < rows;
     f2 v[VPT][4];
+    if constexpr (D > 0) {
+      // the slot read in the iteration before is free: its values are in registers and used
+      fetch(stage == 0 ? D - 1 : stage - 1);
+      cp_async_wait<D - 1>();
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      Vec8<T> p;
-      if constexpr (D > 0) p = Slot8<T>::get(slot0 + (stage * VPT + i) * kVec, B * 16);
-      else load_vec(x, a.ld_x, row, (i * G + t) * 8, a.rows, cols, p);
-      p.get(v[i]);
+      for (int i = 0; i < VPT; ++i) Slot8<T>::get(slot0 + (stage * VPT + i) * kVec, B * 16).get(v[i]);
+      stage = stage >= D - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) load_vec(ahead + i * G * 8, live && in[i]).get(v[i]);
+      ahead += ahead_step;
     }
-    stage = stage >= D - 1 ? 0 : stage + 1;
     f2 p = dup2(0.0f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -152,7 +187,7 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
     for (int i = 0; i < VPT; ++i) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], dup2(-mean));
-      if ((i * G + t) * 8 < cols) {
+      if (in[i]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) p = fma2(v[i][j], v[i][j], p);
       }
@@ -160,24 +195,22 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
     s[0] = p.x + p.y;
     row_sum<G, 1>(s, sh[1]);
     const float rstd = 1.0f / sqrtf(s[0] * a.inv_cols + a.eps);
-    const bool live = row < a.rows;
     if (live && t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * G + t) * 8;
-      const bool in = live && c < cols;
       f2 o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], dup2(rstd)), w[i][j], b[i][j]);
       Vec8<T> q;
       q.set(o);
-      if (in) q.store(static_cast<T*>(a.y) + row * a.ld_y + c);
+      if (live && in[i]) q.store(y + i * G * 8);
       if (a.k.q != nullptr) {
         // the checkpoint is of y as stored; lanes behind the last column hold zeros
-        if (c >= cols) q.zero();
+        const int c = (i * G + t) * 8;
+        if (!in[i]) q.zero();
         const uint32_t amax = q.block_max();
         q.get(o);
         if (live && (c & ~31) < cols) ckpt_store8(a.k, row, c, o, amax);
@@ -226,29 +259,46 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
   const uint32_t base = smem_u32(ring);
   const int t = threadIdx.x % G;
   const int cols = a.cols;
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* x = static_cast<const T*>(a.x);
-  const T* dres = static_cast<const T*>(a.dres);
-  const long long step = (long long)gridDim.x * R;
-  const long long row0 = (long long)blockIdx.x * R + threadIdx.x / G;
+  const uint32_t step = gridDim.x * R, rows = (uint32_t)a.rows;
+  const uint32_t row0 = blockIdx.x * R + threadIdx.x / G;
+  bool in[VPT];  // vectors inside the row
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) in[i] = (i * G + t) * 8 < cols;
+  // where the row ahead and the present row's dx lie, moved on by a step per row
+  const T* dy = static_cast<const T*>(a.dy) + (long long)row0 * a.ld_dy + t * 8;
+  const T* x = KEPT ? nullptr : static_cast<const T*>(a.x) + (long long)row0 * a.ld_x + t * 8;
+  const int8_t* xq = KEPT ? a.k.q + (long long)row0 * a.k.ld_q + t * 8 : nullptr;
+  const T* dres = RES ? static_cast<const T*>(a.dres) + (long long)row0 * a.ld_dres + t * 8 : nullptr;
+  const long long dy_step = (long long)step * a.ld_dy, x_step = (long long)step * (KEPT ? a.k.ld_q : a.ld_x);
+  const long long res_step = (long long)step * a.ld_dres, dx_step = (long long)step * a.ld_dx;
+  T* dx = static_cast<T*>(a.dx) + (long long)row0 * a.ld_dx + t * 8;
+  auto move_on = [&]() {
+    dy += dy_step;
+    if constexpr (KEPT) xq += x_step;
+    else x += x_step;
+    if constexpr (RES) dres += res_step;
+  };
   // a stage: VPT vectors of dy, then of dres, then of x
   auto g_slot = [&](int stage, int i) { return base + stage * kStage + i * kT + threadIdx.x * 16; };
   auto r_slot = [&](int stage, int i) { return base + stage * kStage + (VPT + i) * kT + threadIdx.x * 16; };
   auto x_slot = [&](int stage, int i) {
     return base + stage * kStage + (RES ? 2 : 1) * VPT * kT + i * (Cfg::kX * B) + threadIdx.x * (KEPT ? 8 : 16);
   };
-  auto fetch = [&](long long r, int stage) {
-    if constexpr (D == 0) return;
+  uint32_t row_ahead = row0;
+  auto fetch = [&](int stage) {
+    if (row_ahead < rows) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * G + t) * 8;
-      const bool ok = r < a.rows && c < cols;
-      Slot8<T>::fetch(g_slot(stage, i), B * 16, ok ? dy + r * a.ld_dy + c : dy, ok);
-      if constexpr (KEPT) cp_async8(x_slot(stage, i), ok ? a.k.q + r * a.k.ld_q + c : a.k.q, ok);
-      else Slot8<T>::fetch(x_slot(stage, i), B * 16, ok ? x + r * a.ld_x + c : x, ok);
-      if constexpr (RES) Slot8<T>::fetch(r_slot(stage, i), B * 16, ok ? dres + r * a.ld_dres + c : dres, ok);
+      for (int i = 0; i < VPT; ++i)
+        if (in[i]) {
+          Slot8<T>::fetch(g_slot(stage, i), B * 16, dy + i * G * 8);
+          if constexpr (KEPT) cp_async8(x_slot(stage, i), xq + i * G * 8);
+          else Slot8<T>::fetch(x_slot(stage, i), B * 16, x + i * G * 8);
+          if constexpr (RES) Slot8<T>::fetch(r_slot(stage, i), B * 16, dres + i * G * 8);
+        }
     }
     cp_async_commit();
+    row_ahead += step;
+    move_on();
   };
   // a row's statistics and its blocks' bytes come by plain loads into registers, two rows
   // ahead (one row ahead the loop waited for them)
@@ -256,24 +306,39 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
     float mean, rstd;
     uint32_t e[VPT];
   };
-  auto fetch_small = [&](long long r) {
+  const uint8_t* xe = KEPT ? a.k.e + (long long)row0 * a.k.ld_e + t / 4 : nullptr;
+  const long long e_step = (long long)step * a.k.ld_e;
+  uint32_t row_small = row0;
+  auto fetch_small = [&]() {
     Small q;
-    const bool in = r < a.rows;
-    q.mean = in ? a.mean[r] : 0.0f;
-    q.rstd = in ? a.rstd[r] : 0.0f;
+    const bool ok = row_small < rows;
+    q.mean = ok ? a.mean[row_small] : 0.0f;
+    q.rstd = ok ? a.rstd[row_small] : 0.0f;
     if constexpr (KEPT) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (i * G + t) * 8;
-        q.e[i] = (in && c < cols) ? a.k.e[r * a.k.ld_e + (c >> 5)] : 1u;
-      }
+      for (int i = 0; i < VPT; ++i) q.e[i] = (ok && in[i]) ? xe[i * (G / 4)] : 1u;
+      xe += e_step;
     }
+    row_small += step;
     return q;
   };
+  if constexpr (D > 0) {
+    // slots behind the last column hold zeros for good: dy = 0 there, so every term is 0
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) fetch(row0 + d * step, d);
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (!in[i]) {
+          Slot8<T>::zero(g_slot(d, i), B * 16);
+          if constexpr (KEPT) sts_zero8(x_slot(d, i));
+          else Slot8<T>::zero(x_slot(d, i), B * 16);
+          if constexpr (RES) Slot8<T>::zero(r_slot(d, i), B * 16);
+        }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) fetch(d);
+  }
   launch_dependents();  // the column reduction's blocks, as this kernel's end
-  Small now, next = fetch_small(row0), after = fetch_small(row0 + step);
+  Small now, next = fetch_small(), after = fetch_small();
   f2 w[VPT][4], dw[VPT][4], db[VPT][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -282,74 +347,72 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
     for (int j = 0; j < 4; ++j) w[i][j] = dw[i][j] = db[i][j] = dup2(0.0f);
     if (c < cols) load_param8<T>(a.w, a.w_f32, c, w[i]);
   }
-  long long row = row0;
+  uint32_t row = row0;
   int stage = 0, buf = 0;
-  for (long long r0 = (long long)blockIdx.x * R; r0 < a.rows; r0 += step, row += step, buf ^= 1) {
-    fetch(row + (D - 1) * step, stage == 0 ? D - 1 : stage - 1);
+  for (uint32_t r0 = blockIdx.x * R; r0 < rows; r0 += step, row += step, dx += dx_step, buf ^= 1) {
+    const bool live = row < rows;  // the same for all of a warp
+    if constexpr (D > 0) {
+      fetch(stage == 0 ? D - 1 : stage - 1);
+      cp_async_wait<D - 1>();
+    }
     now = next;
     next = after;
-    after = fetch_small(row + 2 * step);
-    if constexpr (D > 0) cp_async_wait<D - 1>();
-    const bool live = row < a.rows;
-    // where nothing is to be read (columns and rows behind the last) dy is 0, so u and every
-    // sum's term are 0
+    after = fetch_small();
     f2 u[VPT][4], h[VPT][4];
     f2 s0 = dup2(0.0f), s1 = dup2(0.0f);
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * G + t) * 8;
-      Vec8<T> p;
-      if constexpr (D > 0) p = Slot8<T>::get(g_slot(stage, i), B * 16);
-      else load_vec(dy, a.ld_dy, row, c, a.rows, cols, p);
-      p.get(u[i]);
-      if constexpr (KEPT) {
-        CkptVec8 k;
-        if constexpr (D > 0) k.w = lds8(x_slot(stage, i));
-        else k.w = (live && c < cols) ? *reinterpret_cast<const uint2*>(a.k.q + row * a.k.ld_q + c) : make_uint2(0, 0);
-        k.e = now.e[i];
-        k.get(h[i]);
-      } else {
-        if constexpr (D > 0) p = Slot8<T>::get(x_slot(stage, i), B * 16);
-        else load_vec(x, a.ld_x, row, c, a.rows, cols, p);
-        p.get(h[i]);
-      }
+      for (int i = 0; i < VPT; ++i) {
+        if constexpr (D > 0) Slot8<T>::get(g_slot(stage, i), B * 16).get(u[i]);
+        else load_vec(dy + i * G * 8, in[i]).get(u[i]);
+        if constexpr (KEPT) {
+          CkptVec8 k;
+          if constexpr (D > 0) k.w = lds8(x_slot(stage, i));
+          else k.w = in[i] ? *reinterpret_cast<const uint2*>(xq + i * G * 8) : make_uint2(0, 0);
+          k.e = now.e[i];
+          k.get(h[i]);
+        } else {
+          if constexpr (D > 0) Slot8<T>::get(x_slot(stage, i), B * 16).get(h[i]);
+          else load_vec(x + i * G * 8, in[i]).get(h[i]);
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[i][j] = mul2(add2(h[i][j], dup2(-now.mean)), dup2(now.rstd));
-        dw[i][j] = fma2(u[i][j], h[i][j], dw[i][j]);
-        db[i][j] = add2(db[i][j], u[i][j]);
-        u[i][j] = mul2(u[i][j], w[i][j]);
-        s0 = add2(s0, u[i][j]);
-        s1 = fma2(u[i][j], h[i][j], s1);
+        for (int j = 0; j < 4; ++j) {
+          h[i][j] = mul2(add2(h[i][j], dup2(-now.mean)), dup2(now.rstd));
+          dw[i][j] = fma2(u[i][j], h[i][j], dw[i][j]);
+          db[i][j] = add2(db[i][j], u[i][j]);
+          u[i][j] = mul2(u[i][j], w[i][j]);
+          s0 = add2(s0, u[i][j]);
+          s1 = fma2(u[i][j], h[i][j], s1);
+        }
       }
     }
     float s[2] = {s0.x + s0.y, s1.x + s1.y};
     row_sum<G, 2>(s, sh[buf]);
     // rstd (u - mean(u) - h mean(u h))
     const f2 mu = dup2(-s[0] * a.inv_cols), mh = dup2(-s[1] * a.inv_cols);
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * G + t) * 8;
-      f2 o[4];
+      for (int i = 0; i < VPT; ++i) {
+        f2 o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fma2(h[i][j], mh, add2(u[i][j], mu));
-      if constexpr (RES) {
+        for (int j = 0; j < 4; ++j) o[j] = fma2(h[i][j], mh, add2(u[i][j], mu));
+        if constexpr (RES) {
+          f2 r[4];
+          if constexpr (D > 0) Slot8<T>::get(r_slot(stage, i), B * 16).get(r);
+          else load_vec(dres + i * G * 8, in[i]).get(r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = fma2(o[j], dup2(now.rstd), r[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = mul2(o[j], dup2(now.rstd));
+        }
         Vec8<T> p;
-        if constexpr (D > 0) p = Slot8<T>::get(r_slot(stage, i), B * 16);
-        else load_vec(dres, a.ld_dres, row, c, a.rows, cols, p);
-        f2 r[4];
-        p.get(r);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = fma2(o[j], dup2(now.rstd), r[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = mul2(o[j], dup2(now.rstd));
+        p.set(o);
+        if (in[i]) p.store(dx + i * G * 8);
       }
-      Vec8<T> p;
-      p.set(o);
-      if (live && c < cols) p.store(static_cast<T*>(a.dx) + row * a.ld_dx + c);
     }
-    stage = stage >= D - 1 ? 0 : stage + 1;
+    if constexpr (D > 0) stage = stage >= D - 1 ? 0 : stage + 1;
+    else move_on();
   }
   cp_async_wait<0>();
   if (a.part == nullptr) return;
