@@ -89,44 +89,51 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const ActArgs a) {
   };
 #pragma unroll
   for (int d = 0; d < kStages - 1; ++d) fetch(r_begin + 8 * d, d);
-  Bytes e0 = fetch_e(r_begin), e1 = fetch_e(r_begin + 8), e2 = fetch_e(r_begin + 16);
+  // each in its own registers until its row's turn: passed along from row to row they would be
+  // waited for at once
+  Bytes e[kStages];
+#pragma unroll
+  for (int d = 0; d < kStages; ++d) e[d] = fetch_e(r_begin + 8 * d);
   f2 sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = dup2(0.0f);
-  int stage = 0;
-  for (long long r = r_begin; r < r_end; r += 8) {
-    fetch(r + 8 * (kStages - 1), stage == 0 ? kStages - 1 : stage - 1);
-    const Bytes e = e0;
-    e0 = e1, e1 = e2, e2 = fetch_e(r + 24);
-    cp_async_wait<kStages - 1>();
-    const uint32_t src = slot + stage * (kSlot<ACT, KEPT> * kThreads);
-    stage = stage == kStages - 1 ? 0 : stage + 1;
+  for (long long r0 = r_begin; r0 < r_end; r0 += 8 * kStages) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Vec8<T> g;
-      g.w = lds16(src + h * kPiece);
-      f2 d[4];
-      g.get(d);
-      if constexpr (HAS) {
-        f2 f[4];
-        if constexpr (KEPT) {
-          CkptVec8 k;
-          k.w = lds8(src + 2 * kPiece - threadIdx.x * 8 + h * (kPiece / 2));
-          k.e = e.e[h];
-          k.get(f);
-        } else {
-          Vec8<T> v;
-          v.w = lds16(src + (2 + h) * kPiece);
-          v.get(f);
+    for (int stage = 0; stage < kStages; ++stage) {
+      const long long r = r0 + 8 * stage;
+      if (r >= r_end) break;
+      fetch(r + 8 * (kStages - 1), (stage + kStages - 1) % kStages);
+      const Bytes now = e[stage];
+      cp_async_wait<kStages - 1>();
+      const uint32_t src = slot + stage * (kSlot<ACT, KEPT> * kThreads);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        Vec8<T> g;
+        g.w = lds16(src + h * kPiece);
+        f2 d[4];
+        g.get(d);
+        if constexpr (HAS) {
+          f2 f[4];
+          if constexpr (KEPT) {
+            CkptVec8 k;
+            k.w = lds8(src + 2 * kPiece - threadIdx.x * 8 + h * (kPiece / 2));
+            k.e = now.e[h];
+            k.get(f);
+          } else {
+            Vec8<T> v;
+            v.w = lds16(src + (2 + h) * kPiece);
+            v.get(f);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], act_slope<ACT>(f[j]));
+          Vec8<T> o;
+          o.set(d);
+          if (a.dz != nullptr && h < halves) o.store(static_cast<T*>(a.dz) + r * a.ld_dz + c + 256 * h);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], act_slope<ACT>(f[j]));
-        Vec8<T> o;
-        o.set(d);
-        if (a.dz != nullptr && h < halves) o.store(static_cast<T*>(a.dz) + r * a.ld_dz + c + 256 * h);
+        for (int j = 0; j < 4; ++j) sum[4 * h + j] = add2(sum[4 * h + j], d[j]);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[4 * h + j] = add2(sum[4 * h + j], d[j]);
+      e[stage] = fetch_e(r + 8 * kStages);
     }
   }
   cp_async_wait<0>();

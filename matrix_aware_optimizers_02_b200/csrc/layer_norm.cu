@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
     move_on();
   };
   // a row's statistics and its blocks' bytes come by plain loads into registers, two rows
-  // ahead (one row ahead the loop waited for them)
+  // ahead, each row's pair in registers of its own until its turn (passed along from row to row
+  // they would be waited for at once)
   struct Small {
     float mean, rstd;
     uint32_t e[VPT];
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
     for (int d = 0; d < D - 1; ++d) fetch(d);
   }
   launch_dependents();  // the column reduction's blocks, as this kernel's end
-  Small now, next = fetch_small(), after = fetch_small();
+  Small even = fetch_small(), odd = fetch_small();
   f2 w[VPT][4], dw[VPT][4], db[VPT][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -348,16 +349,14 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
     if (c < cols) load_param8<T>(a.w, a.w_f32, c, w[i]);
   }
   uint32_t row = row0;
-  int stage = 0, buf = 0;
-  for (uint32_t r0 = blockIdx.x * R; r0 < rows; r0 += step, row += step, dx += dx_step, buf ^= 1) {
+  int stage = 0;
+  auto body = [&](Small& small, float* sums) {
     const bool live = row < rows;  // the same for all of a warp
     if constexpr (D > 0) {
       fetch(stage == 0 ? D - 1 : stage - 1);
       cp_async_wait<D - 1>();
     }
-    now = next;
-    next = after;
-    after = fetch_small();
+    const Small now = small;
     f2 u[VPT][4], h[VPT][4];
     f2 s0 = dup2(0.0f), s1 = dup2(0.0f);
     if (live) {
@@ -387,7 +386,7 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
       }
     }
     float s[2] = {s0.x + s0.y, s1.x + s1.y};
-    row_sum<G, 2>(s, sh[buf]);
+    row_sum<G, 2>(s, sums);
     // rstd (u - mean(u) - h mean(u h))
     const f2 mu = dup2(-s[0] * a.inv_cols), mh = dup2(-s[1] * a.inv_cols);
     if (live) {
@@ -413,6 +412,15 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
     }
     if constexpr (D > 0) stage = stage >= D - 1 ? 0 : stage + 1;
     else move_on();
+    small = fetch_small();
+    row += step;
+    dx += dx_step;
+  };
+  for (uint32_t r0 = blockIdx.x * R; r0 < rows; r0 += step) {
+    body(even, sh[0]);
+    r0 += step;
+    if (r0 >= rows) break;
+    body(odd, sh[1]);
   }
   cp_async_wait<0>();
   if (a.part == nullptr) return;
