@@ -37,7 +37,8 @@ __global__ void __launch_bounds__(kThreads) ckpt8_kernel(const T* __restrict__ x
       const uint32_t amax = v[u].block_max();  // 4 | vpr: a block's lanes are all in or all out
       f2 f[4];
       v[u].get(f);
-      if (row[u] < st.rows) ckpt_store8(k, row[u], col[u], f, amax);
+      if (row[u] < st.rows)
+        ckpt_store8(k.q + row[u] * k.ld_q + col[u], (col[u] & 31) ? nullptr : k.e + row[u] * k.ld_e + (col[u] >> 5), f, amax);
     }
   }
 }

@@ -431,15 +431,17 @@ struct CkptVec8 {
 // Writes 8 consecutive values' share of a block whose 32 columns are held by 4
 // neighbouring lanes (8 each); amax: the block's largest magnitude (Vec8::block_max).  Lanes
 // behind the last column pass zeros, which become the block's padding.
-__device__ __forceinline__ void ckpt_store8(const CkptView& k, long long row, int c, const f2 (&v)[4], uint32_t amax) {
+// q: where this lane's 8 bytes go; e: where the block's byte goes, for the block's first lane,
+// else nullptr.
+__device__ __forceinline__ void ckpt_store8(int8_t* q, uint8_t* e_out, const f2 (&v)[4], uint32_t amax) {
   const uint32_t e = ckpt_exponent(amax);
   const float inv = ckpt_inverse(e);
   const uint32_t mask = e == 255u ? 0u : 0xffffffffu;
   uint2 w;
   w.x = ckpt_q4(v[0], v[1], inv, mask);
   w.y = ckpt_q4(v[2], v[3], inv, mask);
-  *reinterpret_cast<uint2*>(k.q + row * k.ld_q + c) = w;
-  if ((c & 31) == 0) k.e[row * k.ld_e + (c >> 5)] = (uint8_t)e;
+  *reinterpret_cast<uint2*>(q) = w;
+  if (e_out != nullptr) *e_out = (uint8_t)e;
 }
 
 }  // namespace mao

@@ -103,7 +103,7 @@ struct FwdCfg {
   static constexpr int kSmem = kStages * VPT * Slot8<T>::kBytes * B;
 };
 
-template <class T, int G, int VPT>
+template <class T, bool KEEP, int G, int VPT>
 __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_kernel(const FwdArgs a) {
   using Cfg = FwdCfg<T, G, VPT>;
   constexpr int B = Cfg::B, R = B / G;  // rows per block at a time
@@ -123,6 +123,9 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
   const T* ahead = static_cast<const T*>(a.x) + (long long)row0 * a.ld_x + t * 8;
   const long long ahead_step = (long long)step * a.ld_x, y_step = (long long)step * a.ld_y;
   T* y = static_cast<T*>(a.y) + (long long)row0 * a.ld_y + t * 8;
+  int8_t* kq = a.k.q + (long long)row0 * a.k.ld_q + t * 8;
+  uint8_t* ke = a.k.e + (long long)row0 * a.k.ld_e + t / 4;
+  const long long kq_step = (long long)step * a.k.ld_q, ke_step = (long long)step * a.k.ld_e;
   uint32_t row_ahead = row0;
   auto fetch = [&](int stage) {
     if (row_ahead < rows) {
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
   int stage = 0;
   // the trip count is the block's: rows behind the last take part in the reductions, with
   // whatever their slots hold, and write nothing
-  for (uint32_t r0 = blockIdx.x * R; r0 < rows; r0 += step, row += step, y += y_step) {
+  for (uint32_t r0 = blockIdx.x * R; r0 < rows; r0 += step, row += step, y += y_step, kq += kq_step, ke += ke_step) {
     const bool live = row < rows;
     f2 v[VPT][4];
     if constexpr (D > 0) {
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
     }
     s[0] = p.x + p.y;
     row_sum<G, 1>(s, sh[1]);
-    const float rstd = 1.0f / sqrtf(s[0] * a.inv_cols + a.eps);
+    const float rstd = rsqrtf(s[0] * a.inv_cols + a.eps);  // off by at most 2 steps
     if (live && t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
@@ -207,13 +210,13 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
       Vec8<T> q;
       q.set(o);
       if (live && in[i]) q.store(y + i * G * 8);
-      if (a.k.q != nullptr) {
+      if constexpr (KEEP) {
         // the checkpoint is of y as stored; lanes behind the last column hold zeros
-        const int c = (i * G + t) * 8;
         if (!in[i]) q.zero();
         const uint32_t amax = q.block_max();
         q.get(o);
-        if (live && (c & ~31) < cols) ckpt_store8(a.k, row, c, o, amax);
+        if (live && ((i * G + t) * 8 & ~31) < cols)
+          ckpt_store8(kq + i * G * 8, (t & 3) ? nullptr : ke + i * (G / 4), o, amax);
       }
     }
   }
@@ -520,24 +523,29 @@ int bwd_blocks(int rows, int cols, int sms) {
   return n;
 }
 
-template <class T, int G, int VPT>
+template <class T, bool KEEP, int G, int VPT>
 mao_status fwd_one(const FwdArgs& a, int sms, cudaStream_t stream) {
   using Cfg = FwdCfg<T, G, VPT>;
   static std::atomic<bool> done[64];
-  MAO_TRY(allow_smem(norm_kernel<T, G, VPT>, Cfg::kSmem, done));
+  MAO_TRY(allow_smem(norm_kernel<T, KEEP, G, VPT>, Cfg::kSmem, done));
   const int grid = walk_blocks(a.rows, Cfg::B / G, Cfg::kPerSm, sms);
-  norm_kernel<T, G, VPT><<<grid, Cfg::B, Cfg::kSmem, stream>>>(a);
+  norm_kernel<T, KEEP, G, VPT><<<grid, Cfg::B, Cfg::kSmem, stream>>>(a);
   return launched();
+}
+
+template <class T, bool KEEP>
+mao_status fwd_sized(const FwdArgs& a, int sms, cudaStream_t stream) {
+  const int cols = a.cols;
+  LaunchScope ls(stream, MAO_K_LAYER_NORM, 0.0,
+                 (double)a.rows * cols * (2.0 * sizeof(T) + (KEEP ? 1.0 + 1.0 / 32 : 0.0)));
+#define MAO_CASE(G, V) return fwd_one<T, KEEP, G, V>(a, sms, stream);
+  MAO_NORM_SIZES(MAO_CASE)
+#undef MAO_CASE
 }
 
 template <class T>
 mao_status fwd(const FwdArgs& a, int sms, cudaStream_t stream) {
-  const int cols = a.cols;
-  LaunchScope ls(stream, MAO_K_LAYER_NORM, 0.0,
-                 (double)a.rows * cols * (2.0 * sizeof(T) + (a.k.q ? 1.0 + 1.0 / 32 : 0.0)));
-#define MAO_CASE(G, V) return fwd_one<T, G, V>(a, sms, stream);
-  MAO_NORM_SIZES(MAO_CASE)
-#undef MAO_CASE
+  return a.k.q != nullptr ? fwd_sized<T, true>(a, sms, stream) : fwd_sized<T, false>(a, sms, stream);
 }
 
 template <class T, bool KEPT, bool RES, int G, int VPT>
