@@ -200,8 +200,8 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
     flops += 2.0 * (double)s.M * (double)s.N * (double)s.K;
     j.p[slot] = LinJoin{p.e, p.part, c.tiles_m, c.tiles_n, c.full, c.slices};
     if (c.slices > 1) {
-      // a few rounds of tiles at most: far below 2^31 pieces, a multiple of 128
-      const int k = (c.tiles_m * c.tiles_n - c.full) * (kTileM[plans.tile] * kTileN[plans.tile] / 32);
+      // a few rounds of tiles at most: far below 2^31 pieces, a multiple of a block's
+      const int k = (c.tiles_m * c.tiles_n - c.full) * (kTileM[plans.tile] * kTileN[plans.tile] / 8);
       if (slot == 0) j.pieces = k;
       pieces += k;
     }
@@ -217,11 +217,11 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
   }
   if (pieces == 0) return MAO_OK;
   LaunchScope ls(stream, MAO_K_SLICE_REDUCE, 0.0, (double)plans.part_bytes());
-  const dim3 grid(pieces / 128);
+  const dim3 grid(pieces / kJoinThreads);
   switch (plans.tile) {
-    case TILE_PAIR256: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 256>, grid, 128, 0, stream, j);
-    case TILE_PAIR128: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 128>, grid, 128, 0, stream, j);
-    default: return launch_dependent(lin_join_kernel<T, FORWARD, 128, 128>, grid, 128, 0, stream, j);
+    case TILE_PAIR256: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 256>, grid, kJoinThreads, 0, stream, j);
+    case TILE_PAIR128: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 128>, grid, kJoinThreads, 0, stream, j);
+    default: return launch_dependent(lin_join_kernel<T, FORWARD, 128, 128>, grid, kJoinThreads, 0, stream, j);
   }
 }
 

@@ -165,6 +165,12 @@ __device__ __forceinline__ void act32(float* v) {
   }
 }
 
+template <int ACT>
+__device__ __forceinline__ void act8(f2 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = act_value<ACT>(v[j]);
+}
+
 // 32 consecutive 16-bit elements of one row, `n` of them valid (a multiple of 8)
 template <class T>
 __device__ __forceinline__ void store16x32(T* dst, const float* v, int n) {
@@ -412,6 +418,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
   volatile int* abort_flag = &abort_sh;
+  launch_dependents();  // the joining kernel's blocks, as CTAs of this one end
   if constexpr (!FORWARD) wait_for_previous();  // the operands come from the kernel before
 
   if (warp == 0) {
@@ -634,9 +641,75 @@ __global__ void __launch_bounds__(640, 1) lin_kernel(const __grid_constant__ Lin
   lin_body<T, FORWARD, false, 128>(p);
 }
 
-// Joins the slices of the tails' tiles in slice order and runs the epilogue.  A thread owns
-// 32 columns of a row, as in the product kernel.  pieces: 32-column pieces of the first
-// problem's tail; the second's follow.
+// The same epilogue for 8 columns [col, col + 8) of one row, in a warp whose 4 neighbouring lanes
+// hold the 32 columns of a block; `in` says whether they lie in the matrix.
+template <class T, bool FORWARD>
+__device__ __forceinline__ void lin_epilogue8(const LinEpilogue& e, int row, int col, f2 (&v)[4], bool in) {
+  if constexpr (!FORWARD) {
+    if (!in) return;
+    if (e.kind == LIN_STORE) {
+      Vec8<T> o;
+      o.set(v);
+      o.store(static_cast<T*>(e.out) + (long long)row * e.ld_out + col);
+      return;
+    }
+    float* p = static_cast<float*>(e.out) + (long long)row * e.ld_out + col;
+    Vec8<float> o;
+    if (e.accumulate) {
+      f2 was[4];
+      o.load_keep(p);
+      o.get(was);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = add2(v[j], was[j]);
+    }
+    o.set(v);
+    o.store(p);
+  } else {
+    if (in && e.bias != nullptr) {
+      f2 b[4];
+      load_param8<T>(e.bias, e.bias_f32, col, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = add2(v[j], b[j]);
+    }
+    Vec8<T> o;
+    if (in && e.z != nullptr) {
+      o.set(v);
+      o.store(static_cast<T*>(e.z) + (long long)row * e.ld_z + col);
+    }
+    if (e.k.q != nullptr) {
+      // columns behind the last hold zeros, as in the product kernel
+      Vec8<float> f;
+      f.set(v);
+      const uint32_t amax = f.block_max();
+      if (row < e.M && (col & ~31) < e.N)
+        ckpt_store8(e.k.q + (long long)row * e.k.ld_q + col,
+                    (col & 31) ? nullptr : e.k.e + (long long)row * e.k.ld_e + (col >> 5), v, amax);
+    }
+    if (!in) return;
+    switch (e.act) {
+      case MAO_ACT_RELU: act8<MAO_ACT_RELU>(v); break;
+      case MAO_ACT_RELU2: act8<MAO_ACT_RELU2>(v); break;
+      case MAO_ACT_GELU: act8<MAO_ACT_GELU>(v); break;
+      case MAO_ACT_GELU_TANH: act8<MAO_ACT_GELU_TANH>(v); break;
+      case MAO_ACT_SILU: act8<MAO_ACT_SILU>(v); break;
+      default: break;
+    }
+    if (e.res != nullptr) {
+      f2 r[4];
+      o.load(static_cast<const T*>(e.res) + (long long)row * e.ld_res + col);
+      o.get(r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = add2(v[j], r[j]);
+    }
+    o.set(v);
+    o.store(static_cast<T*>(e.out) + (long long)row * e.ld_out + col);
+  }
+}
+
+// Joins the slices of the sliced tiles in slice order and runs the epilogue.  A thread owns 8
+// columns of a row, so a warp reads whole lines (with 32 columns a thread, as in the product
+// kernel, 22 tiles of 3 slices took 8 us).  pieces: 8-column pieces of the first problem's
+// sliced tiles; the second's follow.
 struct LinJoin {
   LinEpilogue e;
   const float* part;
@@ -647,32 +720,34 @@ struct LinJoins {
   LinJoin p[NP];
   int pieces;
 };
+constexpr int kJoinThreads = 256;
 template <class T, bool FORWARD, int BM, int BN>
-__global__ void __launch_bounds__(128) lin_join_kernel(const LinJoins<FORWARD ? 1 : 2> a) {
+__global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(const LinJoins<FORWARD ? 1 : 2> a) {
   wait_for_previous();
-  int i = blockIdx.x * 128 + threadIdx.x;
-  const bool second = !FORWARD && i >= a.pieces;  // the same for a block: pieces is a multiple of 128
+  int i = blockIdx.x * kJoinThreads + threadIdx.x;
+  const bool second = !FORWARD && i >= a.pieces;  // the same for a block: pieces is a multiple of its size
   if (second) i -= a.pieces;
   const LinJoin& p = a.p[second ? 1 : 0];
-  const int tail = p.tiles_m * p.tiles_n - p.full;
-  const int tile = i / (BM * BN / 32);
-  const int r = i - tile * (BM * BN / 32);
+  const int sliced = p.tiles_m * p.tiles_n - p.full;
+  const int tile = i / (BM * BN / 8);
+  const int r = i - tile * (BM * BN / 8);
   int tm, tn;
   lin_tile(p.full + tile, p.tiles_m, p.tiles_n, tm, tn);
-  const int row = tm * BM + r / (BN / 32), col = tn * BN + (r % (BN / 32)) * 32;
-  if (row >= p.e.M || col >= p.e.N) return;
-  float v[32];
+  const int row = tm * BM + r / (BN / 8), col = tn * BN + (r % (BN / 8)) * 8;
+  const bool in = row < p.e.M && col < p.e.N;
+  f2 v[4] = {dup2(0.0f), dup2(0.0f), dup2(0.0f), dup2(0.0f)};
+  if (in) {
+    const float* s = p.part + (long long)tile * BM * BN + r * 8;
+    for (int k = 0; k < p.slices; ++k, s += (long long)sliced * BM * BN) {
+      Vec8<float> x;
+      x.load(s);
+      f2 f[4];
+      x.get(f);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-  const float* s = p.part + (long long)tile * BM * BN + r * 32;
-  for (int k = 0; k < p.slices; ++k, s += (long long)tail * BM * BN) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(s + j));
-      v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
+      for (int j = 0; j < 4; ++j) v[j] = add2(v[j], f[j]);
     }
   }
-  lin_epilogue<T, FORWARD>(p.e, row, col, v);
+  lin_epilogue8<T, FORWARD>(p.e, row, col, v, in);
 }
 
 }  // namespace mao

@@ -123,12 +123,13 @@ class Checkpoint8:
         self.q, self.e, self.cols, self.dtype = q, e, cols, dtype
 
     @classmethod
-    def empty(cls, rows: int, cols: int, dtype: torch.dtype, device) -> "Checkpoint8":
+    def _like(cls, x: torch.Tensor, rows: int, cols: int) -> "Checkpoint8":
+        """Room for rows x cols of x's type, on its device; nothing to check."""
         blocks = (cols + 31) // 32
-        k = object.__new__(cls)  # nothing to check
-        k.q = torch.empty((rows, 32 * blocks), dtype=torch.int8, device=device)
-        k.e = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
-        k.cols, k.dtype = cols, dtype
+        k = object.__new__(cls)
+        k.q = x.new_empty((rows, 32 * blocks), dtype=torch.int8)
+        k.e = x.new_empty((rows, blocks), dtype=torch.uint8)
+        k.cols, k.dtype = cols, x.dtype
         return k
 
     @property
@@ -173,7 +174,7 @@ def checkpoint8(x: torch.Tensor) -> Checkpoint8:
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return checkpoint8(x)
-    k = Checkpoint8.empty(x.shape[0], x.shape[1], x.dtype, dev)
+    k = Checkpoint8._like(x, x.shape[0], x.shape[1])
     c = k._c()
     L.check(L.load().mao_checkpoint8(x.data_ptr(), _DTYPES[x.dtype], x.shape[0], x.shape[1], ld, ctypes.byref(c),
                                      _stream(dev.index)), "mao_checkpoint8")
@@ -201,7 +202,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
             return layer_norm(x, weight, bias, eps=eps, checkpoint=checkpoint)
     y = x.new_empty((rows, cols))
     mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
-    kept = Checkpoint8.empty(rows, cols, x.dtype, dev) if checkpoint else None
+    kept = Checkpoint8._like(x, rows, cols) if checkpoint else None
     a = L.LayerNormArgs(rows, cols, _DTYPES[x.dtype], _DTYPES[weight.dtype], x.data_ptr(), ld, weight.data_ptr(),
                         _ptr(bias), eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
                         kept._c() if checkpoint else _NO_CKPT)
@@ -297,7 +298,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     if checkpoint == "tensor":
         kept = z = x.new_empty((rows, m))
     elif checkpoint:
-        kept = Checkpoint8.empty(rows, m, dt, dev)
+        kept = Checkpoint8._like(x, rows, m)
         zc = kept._c()
     a = L.LinearArgs(rows, n, m, _DTYPES[dt], x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias),
                      _DTYPES[bias.dtype] if bias is not None else 0, a_id, _ptr(residual), ld_res, y.data_ptr(),
