@@ -370,7 +370,7 @@ __device__ __forceinline__ uint32_t ckpt_exponent(uint32_t amax_bits) {
 __device__ __forceinline__ float ckpt_inverse(uint32_t e) {
   return e == 255u ? 0.0f : __uint_as_float((254u - e) << 23);
 }
-// 2^(e - 127); infinity for a marked block (0 * inf = NaN), 0 for e = 0.
+// 2^(e - 127); 0 for e = 0 (and infinity for a marked block, which ckpt_unpack4 turns into NaN).
 __device__ __forceinline__ float ckpt_scale(uint32_t e) { return __uint_as_float(e << 23); }
 
 // Four bytes of x / step.  x / step is exact; adding 1.5 * 2^23 in the same fma rounds it to
@@ -388,7 +388,8 @@ __device__ __forceinline__ uint32_t ckpt_q4(f2 a, f2 b, float inv, uint32_t mask
 }
 // Four bytes of q to values.  With its sign bit flipped a byte is u = q + 128, and 0x4700uu00
 // is the float 32768 + u; (32768 + u) s - 32896 s = q s in one fma, exactly (q s has 8 bits).
-// 32896 s must stay finite: from s = 2^113 on the subtraction comes first.
+// 32896 s must stay finite: from s = 2^113 on the subtraction comes first.  A marked block is
+// NaN whatever its q.
 __device__ __forceinline__ void ckpt_unpack4(uint32_t w, uint32_t e, f2* v) {
   const float s = ckpt_scale(e);
   const uint32_t u = w ^ 0x80808080u;
@@ -401,8 +402,9 @@ __device__ __forceinline__ void ckpt_unpack4(uint32_t w, uint32_t e, f2* v) {
     v[0] = fma2(a, dup2(s), c);
     v[1] = fma2(b, dup2(s), c);
   } else {
-    v[0] = mul2(add2(a, dup2(-32896.0f)), dup2(s));
-    v[1] = mul2(add2(b, dup2(-32896.0f)), dup2(s));
+    const f2 f = dup2(e == 255u ? __uint_as_float(0x7fffffffu) : s);
+    v[0] = mul2(add2(a, dup2(-32896.0f)), f);
+    v[1] = mul2(add2(b, dup2(-32896.0f)), f);
   }
 }
 
