@@ -282,13 +282,27 @@ struct LinCfg {
   static constexpr int A_TILE = 128 * 128;  // bytes: 128 rows of 64 elements per CTA
   static constexpr int B_TILE = BL * 128;
   static constexpr int STAGE_BYTES = A_TILE + B_TILE;
-  static constexpr int STAGES = STAGE_BYTES > 24 * 1024 ? 6 : 8;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  // As deep as shared memory allows: a stage comes back about 2.3 us after it was asked for (MMAs
+  // done, the commit seen, the load issued, L2, the barrier seen), so the bytes in flight set the
+  // pace of products that the power limit does not: 6 stages 385 ns per k-block, 7 stages 330.
+  static constexpr int STAGES = (224 * 1024) / STAGE_BYTES;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 16;
   static constexpr int COLS = BN / 4;  // columns per epilogue warp
   static constexpr int EPI_FIRST = 4;  // first epilogue warp
   static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
+  // what shared memory holds behind the stages; no static shared memory, so that the stages
+  // start on a 1024-byte boundary without padding
+  struct Shared {
+    uint64_t full_bar[STAGES], empty_bar[STAGES];
+    uint64_t tfull_bar[2], tempty_bar[2];
+    uint64_t drain_bar;
+    uint32_t tmem_base;
+    int abort, prod_it, mma_it;
+    float join[EPI_WARPS][33];
+  };
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + (int)sizeof(Shared);
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Tile -> first row and column: bands of kBandRows tile rows, column by column.
@@ -360,18 +374,12 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
   constexpr int STAGES = Cfg::STAGES, BK = Cfg::BK;
   constexpr int B_MN = FORWARD ? 0 : 1;
 
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[STAGES];
-  __shared__ __align__(8) uint64_t empty_bar[STAGES];
-  __shared__ __align__(8) uint64_t tfull_bar[2];
-  __shared__ __align__(8) uint64_t tempty_bar[2];
-  __shared__ __align__(8) uint64_t drain_bar;
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-  __shared__ int prod_it_sh, mma_it_sh;
-
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  typename Cfg::Shared& sh = *reinterpret_cast<typename Cfg::Shared*>(smem + STAGES * Cfg::STAGE_BYTES);
+  uint64_t* const full_bar = sh.full_bar;
+  uint64_t* const empty_bar = sh.empty_bar;
+  uint64_t* const tfull_bar = sh.tfull_bar;
+  uint64_t* const tempty_bar = sh.tempty_bar;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -379,6 +387,10 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
   const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int workers = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   DevStatus* status = &g_layer_status;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle's unit; the same for every CTA
+    if (threadIdx.x == 0) report(status, MAO_ERR_ALIGN, 50);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -389,19 +401,19 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
       mbar_init(&tfull_bar[a], 1);
       mbar_init(&tempty_bar[a], (PAIR ? 2 : 1) * 32 * Cfg::EPI_WARPS);
     }
-    mbar_init(&drain_bar, 1);
-    abort_sh = 0;
-    prod_it_sh = 0;
-    mma_it_sh = 0;
+    mbar_init(&sh.drain_bar, 1);
+    sh.abort = 0;
+    sh.prod_it = 0;
+    sh.mma_it = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
     __syncwarp();
     if constexpr (PAIR) {
-      tmem_alloc_pair(&tmem_base_sh, Cfg::TMEM_COLS);
+      tmem_alloc_pair(&sh.tmem_base, Cfg::TMEM_COLS);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(&tmem_base_sh, Cfg::TMEM_COLS);
+      tmem_alloc(&sh.tmem_base, Cfg::TMEM_COLS);
       tmem_relinquish();
     }
   }
@@ -416,8 +428,8 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers initialised before any remote arrival
   tc_fence_after();
-  const uint32_t tmem_base = tmem_base_sh;
-  volatile int* abort_flag = &abort_sh;
+  const uint32_t tmem_base = sh.tmem_base;
+  volatile int* abort_flag = &sh.abort;
   launch_dependents();  // the joining kernel's blocks, as CTAs of this one end
   if constexpr (!FORWARD) wait_for_previous();  // the operands come from the kernel before
 
@@ -425,13 +437,12 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
     give_registers();
     if (lane == 0) {
       // -------------------------------------------------------------- producer
-      int it = 0;
+      int it = 0, s = 0;
+      uint32_t ph = 0;
       bool ok = true;
       auto load_item = [&](auto a_mn, const LinProblem& p, const LinItem& t) {
         constexpr int A_MN = decltype(a_mn)::value;
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const int s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1;
           if (!mbar_wait(&empty_bar[s], ph ^ 1, status, 51, abort_flag)) {
             ok = false;
             break;
@@ -447,6 +458,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
           lin_load<PAIR, A_MN, 128>(st, &p.mapA, &full_bar[s], lead, kb * BK, t.m0 + 128 * (int)rank);
           lin_load<PAIR, B_MN, Cfg::BL>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK,
                                         t.n0 + Cfg::BL * (int)rank);
+          if (++s == STAGES) s = 0, ph ^= 1;
         }
       };
       LinWalk<NP> walk(worker, workers);
@@ -456,13 +468,14 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
         if (!FORWARD && p.a_mn) load_item(IntC<1>{}, p, t);
         else load_item(IntC<0>{}, p, t);
       }
-      prod_it_sh = it;
+      sh.prod_it = it;
     }
   } else if (warp == 1) {
     give_registers();
     if (lane == 0 && leader) {
       // -------------------------------------------------------------- MMA issuer
-      int it = 0, used = 0;
+      int it = 0, used = 0, s = 0;
+      uint32_t ph = 0;
       bool ok = true;
       auto mma_item = [&](auto a_mn, const LinItem& t, int fold) {
         constexpr int A_MN = decltype(a_mn)::value;
@@ -479,8 +492,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * Cfg::BN;
           for (int kb = c0; kb < c1; ++kb, ++it) {
-            const int s = it % STAGES;
-            if (!mbar_wait(&full_bar[s], (it / STAGES) & 1, status, 53, abort_flag)) {
+            if (!mbar_wait(&full_bar[s], ph, status, 53, abort_flag)) {
               ok = false;
               break;
             }
@@ -496,6 +508,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
             }
             if constexpr (PAIR) umma_commit_pair(&empty_bar[s], 0x3);
             else umma_commit(&empty_bar[s]);
+            if (++s == STAGES) s = 0, ph ^= 1;
           }
           if (!ok) break;
           if constexpr (PAIR) umma_commit_pair(&tfull_bar[acc], 0x3);
@@ -509,10 +522,10 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
         if (!FORWARD && p.a_mn) mma_item(IntC<1>{}, t, p.fold);
         else mma_item(IntC<0>{}, t, p.fold);
       }
-      mma_it_sh = it;
+      sh.mma_it = it;
       // every MMA issued here has finished before tensor memory is released
-      if constexpr (PAIR) umma_commit_pair(&drain_bar, 0x3);
-      else umma_commit(&drain_bar);
+      if constexpr (PAIR) umma_commit_pair(&sh.drain_bar, 0x3);
+      else umma_commit(&sh.drain_bar);
     }
   } else if (warp < Cfg::EPI_FIRST) {
     give_registers();
@@ -530,7 +543,6 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
     }
     if constexpr (!FORWARD) {
       // 32 columns at a time, the sixteen warps over the parts, joined in a fixed order
-      __shared__ float join[Cfg::EPI_WARPS][33];
       const LinColSum& g = params.sum;
       if (g.out != nullptr) {
         for (int c0 = blockIdx.x * 32; c0 < g.cols; c0 += gridDim.x * 32) {
@@ -546,11 +558,11 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
             }
             for (; i < g.parts; i += 16) s += src[(long long)i * g.cols];
           }
-          join[w][lane] = s;
+          sh.join[w][lane] = s;
           asm volatile("bar.sync 1, 512;" ::: "memory");
           if (w == 0 && c < g.cols) {
 #pragma unroll
-            for (int k = 1; k < Cfg::EPI_WARPS; ++k) s += join[k][lane];
+            for (int k = 1; k < Cfg::EPI_WARPS; ++k) s += sh.join[k][lane];
             g.out[c] = s;
           }
           asm volatile("bar.sync 1, 512;" ::: "memory");
@@ -609,14 +621,14 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
   }
 
   // ------------------------------------------------------------------ teardown
-  if (warp == 1 && lane == 0) mbar_wait(&drain_bar, 0, status, 55, abort_flag, false);
+  if (warp == 1 && lane == 0) mbar_wait(&sh.drain_bar, 0, status, 55, abort_flag, false);
   __syncthreads();
   if (leader && warp == 0 && lane == 0) {
     // after an early exit, let the loads in flight land before the CTA ends: the first
     // CTA's full barriers count both CTAs' bytes, and no producer runs more than STAGES
     // loads ahead of the MMAs
-    const int last = max(prod_it_sh, mma_it_sh + (PAIR && *abort_flag ? STAGES : 0));
-    for (int j = mma_it_sh; j < last; ++j)
+    const int last = max(sh.prod_it, sh.mma_it + (PAIR && *abort_flag ? STAGES : 0));
+    for (int j = sh.mma_it; j < last; ++j)
       mbar_wait(&full_bar[j % STAGES], (j / STAGES) & 1, status, 56, abort_flag, false);
   }
   tc_fence_before();
