@@ -7,8 +7,8 @@ namespace mao {
 namespace {
 
 // ------------------------------------------------------------------ plan
-enum LinTile : int { TILE_PAIR256 = 0, TILE_PAIR128 = 1, TILE_ONE = 2 };
-constexpr int kTileM[3] = {256, 256, 128}, kTileN[3] = {256, 128, 128};
+enum LinTile : int { TILE_PAIR = 0, TILE_ONE = 1 };
+constexpr int kTileEdge[2] = {256, 128};
 constexpr int kPlanSms = 148;
 
 struct Shape {
@@ -40,19 +40,23 @@ bool cut(LinPlan& p, int whole, int s, int tile_bytes) {
 // first), from their sizes alone (and so the same on every device and in the workspace
 // query): of the candidates, the one whose longest list is estimated to end first.
 bool search_plan(const Shape* q, int n, LinPlans* out) {
-  // ns, measured: a k-block of 64; set-up, first loads and last epilogue; the joining kernel
-  constexpr double kBlock[3] = {385.0, 300.0, 320.0}, kFixed[3] = {6500.0, 5500.0, 5000.0};
-  constexpr double kJoin = 3500.0, kJoinBytes = 4000.0;  // its launch; bytes per ns, written and read
+  // ns, fitted to products forced onto either tile, of 33 x 768 -> 2304 to 4001 x 6144 -> 1536,
+  // whole and in 2 to 8 slices: a k-block of 64; set-up, first loads and last epilogue; and an
+  // item's own share, in k-blocks.  E.g. 2048 x 768 -> 768: 10.5 us in 128 x 128 tiles, 14.6 in
+  // 256 x 256; 4001 x 6144 -> 1536: 90 and 61 us; 512 x 4096 -> 4096: 27 and 27 us (in 2 slices)
+  constexpr double kBlock[2] = {310.0, 285.0}, kFixed[2] = {7000.0, 7000.0};
+  constexpr long long kItem[2] = {8, 4};
+  constexpr double kJoin = 2500.0, kJoinBytes = 6000.0;  // the joining kernel; bytes per ns, written and read
   constexpr int kSlices[8] = {1, 2, 3, 4, 6, 8, 12, 16};
   double best = 1e300;
-  for (int t = 0; t < 3; ++t) {
+  for (int t = 0; t < 2; ++t) {
     const long long W = t == TILE_ONE ? kPlanSms : kPlanSms / 2;
-    const int tile_bytes = 4 * kTileM[t] * kTileN[t];
+    const int tile_bytes = 4 * kTileEdge[t] * kTileEdge[t];
     LinPlans c;
     c.tile = t;
     bool fits = true;
     for (int i = 0; i < n; ++i) {
-      const long long tm = (q[i].M + kTileM[t] - 1) / kTileM[t], tn = (q[i].N + kTileN[t] - 1) / kTileN[t];
+      const long long tm = (q[i].M + kTileEdge[t] - 1) / kTileEdge[t], tn = (q[i].N + kTileEdge[t] - 1) / kTileEdge[t];
       fits = fits && tm * tn <= (1ll << 26);
       c.p[i].tiles_m = (int)tm, c.p[i].tiles_n = (int)tn;
       c.p[i].nk = (int)((q[i].K + 63) / 64);
@@ -64,9 +68,9 @@ bool search_plan(const Shape* q, int n, LinPlans* out) {
     for (int s0 : kSlices) {
       if (s0 > 1 && (n == 1 || tiles0 >= W)) break;  // the first is cut as a whole, where it is small
       if (n > 1 && !cut(c.p[0], s0 > 1 ? 0 : (int)tiles0, s0, tile_bytes)) continue;
-      const long long first = tiles0 * s0, len0 = n > 1 ? c.p[0].slice_blocks : 0;
+      const long long first = tiles0 * s0, len0 = n > 1 ? c.p[0].slice_blocks + kItem[t] : 0;
       const long long extra = first % W, others = W - extra, base = first / W * len0;
-      const long long len1 = last.nk;
+      const long long len1 = last.nk + kItem[t];
       // whole items of the last problem per list, so that the lists end about together
       const long long total = first * len0 + tiles1 * len1;
       const long long y0 = std::max(0ll, (total / W - base) / len1), x0 = std::max(0ll, (total / W - base - len0) / len1);
@@ -78,7 +82,7 @@ bool search_plan(const Shape* q, int n, LinPlans* out) {
           for (int s1 : kSlices) {
             if (s1 > 1 && rest == 0) break;
             if (!cut(last, s1 > 1 ? (int)whole : (int)tiles1, s1, tile_bytes)) continue;
-            const long long cuts = rest * s1, len = last.slice_blocks;
+            const long long cuts = rest * s1, len = last.slice_blocks + kItem[t];
             const long long most = (cuts + others - 1) / others;
             for (long long v = extra > 0 ? 0 : most; v <= std::min(most, 40ll) || extra == 0; ++v) {
               const long long u = extra > 0 ? (std::max(0ll, cuts - others * v) + extra - 1) / extra : 0;
@@ -129,12 +133,12 @@ bool plan_of(const Shape* q, int n, LinPlans* out) {
 }
 
 // ------------------------------------------------------------------ launch
-template <class T, bool FORWARD, bool PAIR, int BN>
+template <class T, bool FORWARD, bool PAIR>
 mao_status launch_product(const LinParams<FORWARD ? 1 : 2>& p, int items, bool dependent, const DeviceInfo& dev,
                           cudaStream_t stream) {
-  using Cfg = LinCfg<PAIR, BN>;
+  using Cfg = LinCfg<PAIR>;
   void (*kern)(LinParams<FORWARD ? 1 : 2>);
-  if constexpr (PAIR) kern = lin_pair_kernel<T, FORWARD, BN>;
+  if constexpr (PAIR) kern = lin_pair_kernel<T, FORWARD>;
   else kern = lin_kernel<T, FORWARD>;
   static std::atomic<bool> done[64];
   MAO_TRY(allow_smem(kern, Cfg::SMEM_BYTES, done));
@@ -150,11 +154,11 @@ struct Operand {
   long long inner, rows, ld;  // stored matrix: rows x inner
 };
 
-// box_rows: the rows of a K-major tile that one CTA loads
-mao_status encode(CUtensorMap* map, int dtype, const Operand& o, bool mn, int box_rows) {
+// K-major: boxes of 128 rows; MN-major: of 64 columns
+mao_status encode(CUtensorMap* map, int dtype, const Operand& o, bool mn) {
   return encode_3d(map, dtype == MAO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, o.p,
                    (uint64_t)o.inner, (uint64_t)o.rows, 1, (uint64_t)o.ld, (uint64_t)o.ld * o.rows, 64,
-                   mn ? 64 : box_rows);
+                   mn ? 64 : 128);
 }
 
 // One product of a launch: out = A B^T with the stored operands as described.
@@ -185,8 +189,8 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
     const LinPlan& c = plans.p[i];
     const int slot = i + NP - n;  // a single product of the backward pass is its kernel's last
     LinProblem& p = a.p[slot];
-    MAO_TRY(encode(&p.mapA, Elem<T>::kDtype, q[i].A, q[i].a_mn, 128));
-    MAO_TRY(encode(&p.mapB, Elem<T>::kDtype, q[i].B, !FORWARD, plans.tile == TILE_PAIR128 ? 64 : 128));
+    MAO_TRY(encode(&p.mapA, Elem<T>::kDtype, q[i].A, q[i].a_mn));
+    MAO_TRY(encode(&p.mapB, Elem<T>::kDtype, q[i].B, !FORWARD));
     p.e = q[i].e;
     p.part = part;
     part += c.part_bytes / sizeof(float);
@@ -201,7 +205,7 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
     j.p[slot] = LinJoin{p.e, p.part, c.tiles_m, c.tiles_n, c.full, c.slices};
     if (c.slices > 1) {
       // a few rounds of tiles at most: far below 2^31 pieces, a multiple of a block's
-      const int k = (c.tiles_m * c.tiles_n - c.full) * (kTileM[plans.tile] * kTileN[plans.tile] / 8);
+      const int k = (c.tiles_m * c.tiles_n - c.full) * (kTileEdge[plans.tile] * kTileEdge[plans.tile] / 8);
       if (slot == 0) j.pieces = k;
       pieces += k;
     }
@@ -209,20 +213,15 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
   if (n < NP) a.p[0].mapA = a.p[NP - 1].mapA, a.p[0].mapB = a.p[NP - 1].mapB;  // prefetched, not used
   {
     LaunchScope ls(stream, kernel_id, flops, bytes);
-    switch (plans.tile) {
-      case TILE_PAIR256: MAO_TRY((launch_product<T, FORWARD, true, 256>(a, items, dependent, *dev, stream))); break;
-      case TILE_PAIR128: MAO_TRY((launch_product<T, FORWARD, true, 128>(a, items, dependent, *dev, stream))); break;
-      default: MAO_TRY((launch_product<T, FORWARD, false, 128>(a, items, dependent, *dev, stream))); break;
-    }
+    MAO_TRY(plans.tile == TILE_PAIR ? (launch_product<T, FORWARD, true>(a, items, dependent, *dev, stream))
+                                    : (launch_product<T, FORWARD, false>(a, items, dependent, *dev, stream)));
   }
   if (pieces == 0) return MAO_OK;
   LaunchScope ls(stream, MAO_K_SLICE_REDUCE, 0.0, (double)plans.part_bytes());
   const dim3 grid(pieces / kJoinThreads);
-  switch (plans.tile) {
-    case TILE_PAIR256: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 256>, grid, kJoinThreads, 0, stream, j);
-    case TILE_PAIR128: return launch_dependent(lin_join_kernel<T, FORWARD, 256, 128>, grid, kJoinThreads, 0, stream, j);
-    default: return launch_dependent(lin_join_kernel<T, FORWARD, 128, 128>, grid, kJoinThreads, 0, stream, j);
-  }
+  return plans.tile == TILE_PAIR
+             ? launch_dependent(lin_join_kernel<T, FORWARD, 256>, grid, kJoinThreads, 0, stream, j)
+             : launch_dependent(lin_join_kernel<T, FORWARD, 128>, grid, kJoinThreads, 0, stream, j);
 }
 
 LinEpilogue epilogue(void* out, long long ld, int M, int N, int kind) {

@@ -15,10 +15,11 @@
 // is 640 * 96).  With eight epilogue warps and 128 running sums a thread the epilogue, not the
 // MMAs, set the pace of products of few k-blocks.
 //
-// Tiles.  PAIR: 256 x BN per CTA pair (tcgen05.mma.cta_group::2); each CTA loads 128 rows
-// of A and half of B's BN.  BN = 256 streams 64 operand bytes per clock of tensor work, which
-// leaves shared memory room to refill; BN = 128 is for products whose 256 x 256 tiles leave
-// SMs idle.  One CTA: 128 x 128, for products of up to 128 rows.
+// Tiles.  PAIR: 256 x 256 per CTA pair (tcgen05.mma.cta_group::2); each CTA loads 128 rows of A
+// and half of B's 256, for twice the MMA work of a one-CTA 128 x 128 tile's loads.  Either way a
+// CTA takes in 32 KB per k-block at about 110 GB/s, the rate at which an SM's loads arrive, so
+// the one-CTA tile is for products whose 256 x 256 tiles would leave SMs idle.  (256 x 128 pair
+// tiles were measured and dropped: 24 KB per k-block took as long, no size gained.)
 // Tiles that do not fill a whole round of the workers may be cut into K slices: each slice
 // leaves its fp32 sums of the tile in the workspace, and a second kernel joins them in slice
 // order and runs the same epilogue.
@@ -273,18 +274,17 @@ __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int 
 }
 
 // ------------------------------------------------------------------ kernel
-template <bool PAIR, int BN_>
+template <bool PAIR>
 struct LinCfg {
   static constexpr int BM = PAIR ? 256 : 128;  // tile rows (128 per CTA)
-  static constexpr int BN = BN_;               // tile columns
-  static constexpr int BL = PAIR ? BN / 2 : BN;  // B rows loaded by a CTA
+  static constexpr int BN = PAIR ? 256 : 128;  // tile columns
   static constexpr int BK = 64;
   static constexpr int A_TILE = 128 * 128;  // bytes: 128 rows of 64 elements per CTA
-  static constexpr int B_TILE = BL * 128;
+  static constexpr int B_TILE = 128 * 128;  // PAIR: half of B's rows per CTA
   static constexpr int STAGE_BYTES = A_TILE + B_TILE;
   // As deep as shared memory allows: a stage comes back about 2.3 us after it was asked for (MMAs
   // done, the commit seen, the load issued, L2, the barrier seen), so the bytes in flight set the
-  // pace of products that the power limit does not: 6 stages 385 ns per k-block, 7 stages 330.
+  // pace of products that the power limit does not (4096^3: 118 us with 6 stages, 108 with 7).
   static constexpr int STAGES = (224 * 1024) / STAGE_BYTES;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 16;
@@ -351,8 +351,8 @@ __device__ __forceinline__ LinItem lin_item(const LinProblem& p, int item) {
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 32;"); }
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 112;"); }
 
-// One operand's share of a stage: R rows (K-major) or R columns of 64 K rows (MN-major).
-template <bool PAIR, int MN_MAJOR, int R>
+// One operand's share of a stage: 128 rows (K-major) or 128 columns of 64 K rows (MN-major).
+template <bool PAIR, int MN_MAJOR>
 __device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t bar_lead,
                                          int k0, int mn0) {
   if constexpr (!MN_MAJOR) {
@@ -360,17 +360,17 @@ __device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* map, u
     else tma_load_3d(dst, map, bar, k0, mn0, 0);
   } else {
 #pragma unroll
-    for (int c = 0; c < R / 64; ++c) {
+    for (int c = 0; c < 2; ++c) {
       if constexpr (PAIR) tma_load_3d_pair(dst + c * 64 * 128, map, bar_lead, mn0 + c * 64, k0, 0);
       else tma_load_3d(dst + c * 64 * 128, map, bar, mn0 + c * 64, k0, 0);
     }
   }
 }
 
-template <class T, bool FORWARD, bool PAIR, int BN>
+template <class T, bool FORWARD, bool PAIR>
 __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& params) {
   constexpr int NP = FORWARD ? 1 : 2;
-  using Cfg = LinCfg<PAIR, BN>;
+  using Cfg = LinCfg<PAIR>;
   constexpr int STAGES = Cfg::STAGES, BK = Cfg::BK;
   constexpr int B_MN = FORWARD ? 0 : 1;
 
@@ -455,9 +455,9 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
           } else {
             mbar_arrive_expect_tx(&full_bar[s], Cfg::STAGE_BYTES);
           }
-          lin_load<PAIR, A_MN, 128>(st, &p.mapA, &full_bar[s], lead, kb * BK, t.m0 + 128 * (int)rank);
-          lin_load<PAIR, B_MN, Cfg::BL>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK,
-                                        t.n0 + Cfg::BL * (int)rank);
+          lin_load<PAIR, A_MN>(st, &p.mapA, &full_bar[s], lead, kb * BK, t.m0 + 128 * (int)rank);
+          lin_load<PAIR, B_MN>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK,
+                                        t.n0 + 128 * (int)rank);
           if (++s == STAGES) s = 0, ph ^= 1;
         }
       };
@@ -501,7 +501,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
             const uint32_t b_base = a_base + Cfg::A_TILE;
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
-              const uint64_t ad = operand_desc<A_MN, 128, 2>(a_base, k), bd = operand_desc<B_MN, Cfg::BL, 2>(b_base, k);
+              const uint64_t ad = operand_desc<A_MN, 128, 2>(a_base, k), bd = operand_desc<B_MN, 128, 2>(b_base, k);
               const uint32_t accum = (kb > c0 || k > 0) ? 1u : 0u;
               if constexpr (PAIR) umma_f16_pair(d_tmem, ad, bd, IDESC, accum);
               else umma_f16(d_tmem, ad, bd, IDESC, accum);
@@ -642,15 +642,15 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
   }
 }
 
-template <class T, bool FORWARD, int BN>
+template <class T, bool FORWARD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(640, 1)
     lin_pair_kernel(const __grid_constant__ LinParams<FORWARD ? 1 : 2> p) {
-  lin_body<T, FORWARD, true, BN>(p);
+  lin_body<T, FORWARD, true>(p);
 }
 
 template <class T, bool FORWARD>
 __global__ void __launch_bounds__(640, 1) lin_kernel(const __grid_constant__ LinParams<FORWARD ? 1 : 2> p) {
-  lin_body<T, FORWARD, false, 128>(p);
+  lin_body<T, FORWARD, false>(p);
 }
 
 // The same epilogue for 8 columns [col, col + 8) of one row, in a warp whose 4 neighbouring lanes
@@ -733,8 +733,9 @@ struct LinJoins {
   int pieces;
 };
 constexpr int kJoinThreads = 256;
-template <class T, bool FORWARD, int BM, int BN>
+template <class T, bool FORWARD, int EDGE>
 __global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(const LinJoins<FORWARD ? 1 : 2> a) {
+  constexpr int BM = EDGE, BN = EDGE;
   wait_for_previous();
   int i = blockIdx.x * kJoinThreads + threadIdx.x;
   const bool second = !FORWARD && i >= a.pieces;  // the same for a block: pieces is a multiple of its size
