@@ -2,9 +2,10 @@
 
     python -m matrix_aware_optimizers_02_b200.build [--force] [-j N]
 
-Each .cu under csrc/ compiles to an object in _build/ (in parallel), then one
-shared library is linked with the static CUDA runtime.  The driver API is
-reached through cudaGetDriverEntryPoint, so nothing links against libcuda.
+Each .cu under csrc/ and csrc/layers/ (the trained-layer operators) compiles to an
+object in _build/ (in parallel), then one shared library is linked with the static
+CUDA runtime.  The driver API is reached through cudaGetDriverEntryPoint, so nothing
+links against libcuda.
 """
 
 from __future__ import annotations
@@ -41,11 +42,12 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "layers", "*.cu")))
 
 
 def _deps():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu*")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  glob.glob(os.path.join(CSRC, "layers", "*.cu*")) + glob.glob(os.path.join(CSRC, "layers", "*.h")) +
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
