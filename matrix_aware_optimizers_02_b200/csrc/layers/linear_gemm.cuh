@@ -33,12 +33,12 @@
 // Order.  Tiles run in bands of kBandRows tile rows, column by column inside a band, so the
 // tiles that are in flight together share few operand rows and columns in L2.
 //
-// Accuracy.  The tensor core's accumulation truncates: its error grows with every add (a 4096
-// K of random terms: 2e-6 of the sum).  Results of 16 bits accumulate the whole K.  An fp32 dW,
-// and a forward product whose z is kept in 8 bits (where a sum's error decides which way a
-// value rounds), accumulate kFoldBlocks * 64 of K in tensor memory at a time, and the epilogue
-// adds those sums in fp32 registers, rounded to nearest: 1e-6, for 3 to 5 % of the time, the
-// tensor memory's reads.
+// Accuracy.  The tensor core's accumulation truncates: a sum over K terms of random sign is off by
+// 1e-6 of its size for every 1024 of K, where fp32 with rounding stays below 1e-6.  Results of
+// 16 bits accumulate the whole K.  An fp32 dW, and a forward product whose z is kept in 8 bits
+// (where a sum's error decides which way a value rounds), accumulate 12 and 16 k-blocks in tensor
+// memory at a time, and the epilogue adds those sums in fp32 registers, rounded to nearest: 7e-7
+// and 1e-6 for any K.  Reading an accumulator holds the MMAs up for 0.4 us, 6 % at 16 blocks.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -50,7 +50,7 @@ namespace mao {
 static __device__ DevStatus g_layer_status;
 
 constexpr int kBandRows = 8;
-constexpr int kFoldBlocks = 16;
+constexpr int kFoldGrad = 12, kFoldKept = 16;
 
 // Epilogues of the backward kernel; the forward kernel has its own (bias, activation,
 // residual, checkpoint of z).
@@ -172,6 +172,24 @@ __device__ __forceinline__ void act8(f2 (&v)[4]) {
   for (int j = 0; j < 4; ++j) v[j] = act_value<ACT>(v[j]);
 }
 
+__device__ __forceinline__ void ld_global_v8(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+// v += 16 consecutive 16-bit elements, a whole sector in one load
+template <class T>
+__device__ __forceinline__ void add16x16(const T* src, float* v) {
+  uint32_t w[8];
+  ld_global_v8(src, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const f2 f = Elem<T>::unpack(w[i]);
+    v[2 * i] += f.x, v[2 * i + 1] += f.y;
+  }
+}
+
 // 32 consecutive 16-bit elements of one row, `n` of them valid (a multiple of 8)
 template <class T>
 __device__ __forceinline__ void store16x32(T* dst, const float* v, int n) {
@@ -258,16 +276,21 @@ __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int 
     }
     if (e.res != nullptr) {
       const T* r = static_cast<const T*>(e.res) + (long long)row * e.ld_res + col;
+      if (n == 32 && aligned32(r)) {
+        add16x16(r, v);
+        add16x16(r + 16, v + 16);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 32; j += 8)
-        if (j < n) {
-          Vec8<T> x;
-          x.load(r + j);
-          f2 f[4];
-          x.get(f);
+        for (int j = 0; j < 32; j += 8)
+          if (j < n) {
+            Vec8<T> x;
+            x.load(r + j);
+            f2 f[4];
+            x.get(f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[j + 2 * i] += f[i].x, v[j + 2 * i + 1] += f[i].y;
-        }
+            for (int i = 0; i < 4; ++i) v[j + 2 * i] += f[i].x, v[j + 2 * i + 1] += f[i].y;
+          }
+      }
     }
     store16x32<T>(static_cast<T*>(e.out) + (long long)row * e.ld_out + col, v, n);
   }
@@ -576,6 +599,12 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
       const LinProblem& p = params.p[which];
       const LinItem t = lin_item<Cfg>(p, item);
       const int row = t.m0 + 128 * (int)rank + q * 32 + lane;
+      if constexpr (FORWARD) {
+        // the residual's lines (128 bytes of this thread's row) on their way to L2 meanwhile
+        if (p.e.res != nullptr && t.part < 0 && row < p.e.M && t.n0 + cb < p.e.N)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(p.e.res) + (long long)row * p.e.ld_res +
+                                                        t.n0 + cb));
+      }
       float run[COLS];
       for (int c0 = t.kb0; c0 < t.kb1; c0 += p.fold) {
         const int acc = used & 1;
