@@ -207,9 +207,12 @@ __device__ __forceinline__ void store16x32(T* dst, const float* v, int n) {
 }
 
 // The epilogue of 32 consecutive columns [col, col + 32) of one row; v holds the sums.
-// Columns come in eights (N is a multiple of 8).
-template <class T, bool FORWARD>
-__device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int col, float* v) {
+// Columns come in eights (N is a multiple of 8).  With PAIRS a warp's columns come as pairs of
+// such pieces: `second` says which, and `e_first` carries the first's checkpoint byte to the
+// second, so that a lane writes two bytes at once (each lane's lie in a line of their own).
+template <class T, bool FORWARD, bool PAIRS>
+__device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int col, float* v, bool second,
+                                             uint32_t& e_first) {
   if (row >= e.M || col >= e.N) return;
   const int n = min(32, e.N - col);
   if constexpr (!FORWARD) {
@@ -264,7 +267,15 @@ __device__ __forceinline__ void lin_epilogue(const LinEpilogue& e, int row, int 
         reinterpret_cast<uint4*>(q)[0] = make_uint4(w[0], w[1], w[2], w[3]);
         reinterpret_cast<uint4*>(q)[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
-      e.k.e[(long long)row * e.k.ld_e + (col >> 5)] = (uint8_t)ex;
+      uint8_t* eb = e.k.e + (long long)row * e.k.ld_e + (col >> 5);
+      if (!second) {
+        e_first = ex;
+        if (!PAIRS || col + 32 >= e.N) *eb = (uint8_t)ex;  // no second, or the row ends here
+      } else if ((reinterpret_cast<uintptr_t>(eb - 1) & 1u) == 0) {
+        *reinterpret_cast<uint16_t*>(eb - 1) = (uint16_t)(e_first | ex << 8);
+      } else {
+        eb[-1] = (uint8_t)e_first, eb[0] = (uint8_t)ex;
+      }
     }
     switch (e.act) {
       case MAO_ACT_RELU: act32<MAO_ACT_RELU>(v); break;
@@ -632,6 +643,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
       if (!ok) break;
       // The chunks of 32 columns through one copy of the epilogue's code (unrolled, it would
       // be fetched anew for every chunk of a short product): the sums move down by a chunk.
+      uint32_t e_first = 0;
 #pragma unroll 1
       for (int ch = 0; ch < COLS / 32; ++ch) {
         float v[32];
@@ -643,7 +655,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
           // all of a sliced tile is stored, what lies behind the matrix too: zeros
           store_f32x32(p.part + ((long long)t.part * Cfg::BM + (row - t.m0)) * Cfg::BN + cb + ch * 32, v);
         } else {
-          lin_epilogue<T, FORWARD>(p.e, row, t.n0 + cb + ch * 32, v);
+          lin_epilogue<T, FORWARD, COLS == 64>(p.e, row, t.n0 + cb + ch * 32, v, ch & 1, e_first);
         }
       }
     }
