@@ -2,7 +2,8 @@
  * mao.h — C ABI of libmao: one optimizer step of the matrix-aware optimizers
  * Muon (with the optional Muon+ normalisation), two-sided SOAP with a per-step
  * power-iteration/QR eigenbasis refresh, and one-sided factored FOAM, applied
- * to a batch of weight matrices on one B200 GPU (sm_100a).
+ * to a batch of weight matrices on one B200 GPU (sm_100a); and the trained layers
+ * that make those matrices' gradients ("trained layers" below).
  *
  * Sources of the operations (page title, section):
  *   "SOAP, Muon and Beyond" review: 1-1 Problem definition (Shampoo factors
@@ -314,7 +315,8 @@ MAO_API mao_status mao_foam_step(const mao_foam_mat* mats, int32_t count, const 
  *   - A matrix of activations is rows x cols, a row per token, row-major with a leading
  *     dimension `ld` >= cols (elements).  Its elements are of type `dtype`; cols and ld are
  *     multiples of 8 and its base is 16-byte aligned, so that every row is.  rows may be
- *     any number from 0; rows behind the last are not touched.
+ *     any number from 0; rows behind the last are not touched.  rows and cols are at most
+ *     2^30 (MAO_ERR_SHAPE above that).
  *   - With rows = 0 a forward call does nothing, and a backward call writes zeros to the
  *     weight's and the bias's gradient (adds nothing, where it accumulates).
  *   - Products, sums and statistics are held in fp32; results are rounded once to their

@@ -20,8 +20,11 @@ inline mao_status check_acts(const void* p, int rows, int cols, long long ld) {
   if (ld < cols || (ld & 7) || ld > (1ll << 36)) return MAO_ERR_SHAPE;
   return aligned16(p) ? MAO_OK : MAO_ERR_ALIGN;
 }
+// at most 2^30 each way: row and column numbers rounded up to a tile, or a grid past the end,
+// stay in 32 bits
 inline mao_status check_dims(int rows, int cols) {
-  return (rows < 0 || cols < 1 || (cols & 7)) ? MAO_ERR_SHAPE : MAO_OK;
+  constexpr int most = 1 << 30;
+  return (rows < 0 || rows > most || cols < 1 || cols > most || (cols & 7)) ? MAO_ERR_SHAPE : MAO_OK;
 }
 inline mao_status check_ckpt(const mao_ckpt8& c, int rows, int cols) {
   if (rows > 0 && (c.q == nullptr || c.e == nullptr)) return MAO_ERR_INVALID_ARG;

@@ -28,6 +28,7 @@ from . import _lib as L
 
 _DTYPES = {torch.float32: L.MAO_F32, torch.bfloat16: L.MAO_BF16, torch.float16: L.MAO_F16}
 _HALF = (torch.bfloat16, torch.float16)
+_MOST = 2**30
 _NO_CKPT = L.Ckpt8(None, None, 0, 0)
 
 
@@ -54,6 +55,8 @@ def _check_acts(name: str, t: torch.Tensor, shape=None, device=None, dtype=None)
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if cols % 8 or cols == 0:
         raise ValueError(f"{name} has {cols} columns: a positive multiple of 8 is needed")
+    if max(rows, cols) > _MOST:  # above 32 bits the C structs' fields would cut it without an error
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: at most {_MOST} rows and columns")
     if rows > 1:
         ld = t.stride(0)
         if t.stride(1) != 1 or ld < cols or ld % 8:

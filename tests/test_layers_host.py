@@ -169,3 +169,27 @@ def test_python_refuses_host_tensors_and_bad_names():
         api.Checkpoint8(None, None, 16, torch.int32)
     with pytest.raises(ValueError):
         api.Checkpoint8(None, None, 12, torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", [2**30 + 1, 2**31, 2**32 + 5])
+def test_row_counts_past_the_limit_are_refused(monkeypatch, rows):
+    """2^32 + 5 rows must not reach the C structs, whose 32-bit fields would make 5 of them."""
+    from matrix_aware_optimizers_02_b200 import layers
+    monkeypatch.setattr(layers, "_check", lambda *a, **k: None)
+    x = torch.empty((rows, 8), dtype=torch.bfloat16, device="meta")
+    for call in (lambda: layers.checkpoint8(x), lambda: layers.layer_norm(x, x), lambda: layers.linear(x, x),
+                 lambda: layers.layer_norm_backward(x, x, x, x, x), lambda: layers.linear_backward(x, x, x)):
+        with pytest.raises(ValueError, match="at most"):
+            call()
+
+
+def test_entry_points_refuse_sizes_past_the_limit(lib):
+    big = 2**30 + 8
+    k = L.Ckpt8(A16, A16, 32, 1)
+    assert lib.mao_checkpoint8(A16, L.MAO_BF16, big, 8, 8, ctypes.byref(k), None) == L.MAO_ERR_SHAPE
+    a = L.LinearArgs(4, 8, 8, L.MAO_BF16, A16, 8, A16, None, 0, 0, None, 0, A16, 8, None, 8, NONE)
+    n = ctypes.c_size_t(0)
+    assert lib.mao_linear_workspace_size(ctypes.byref(a), ctypes.byref(n)) == L.MAO_OK
+    for kw in (dict(rows=big), dict(n=big), dict(m=big)):
+        b = L.LinearArgs(*[getattr(a, f[0]) for f in a._fields_])
+        assert lib.mao_linear_workspace_size(ctypes.byref(_set(b, **kw)), ctypes.byref(n)) == L.MAO_ERR_SHAPE
