@@ -198,7 +198,7 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
     p.tiles_m = c.tiles_m, p.tiles_n = c.tiles_n;
     p.full = c.full, p.slices = c.slices;
     p.nk = c.nk, p.slice_blocks = c.slice_blocks;
-    p.fold = p.e.kind == LIN_GRAD32 ? kFoldGrad : (p.e.k.q != nullptr ? kFoldKept : p.nk);
+    p.fold = p.e.kind == LIN_GRAD32 || p.e.k.q != nullptr ? kFold : p.nk;
     items += c.items();
     const Shape s = q[i].shape();
     flops += 2.0 * (double)s.M * (double)s.N * (double)s.K;

@@ -12,8 +12,9 @@
 //   warps 4-19  epilogue, four per tensor-memory lane quarter, a quarter of the columns each.
 // Two accumulators let an item's epilogue overlap the next item's MMAs.  The first four warps
 // hand registers to the epilogue (32 against 112 a thread, 96 at launch: 128 * 32 + 512 * 112
-// is 640 * 96).  With eight epilogue warps and 128 running sums a thread the epilogue, not the
-// MMAs, set the pace of products of few k-blocks.
+// is 640 * 96); without that 4096 x 1536 -> 1536 took 36.9 instead of 32.8 us.  Sixteen epilogue
+// warps hold the running sums of a 128 x 256 accumulator in 64 registers a thread; eight would
+// need 128.
 //
 // Tiles.  PAIR: 256 x 256 per CTA pair (tcgen05.mma.cta_group::2); each CTA loads 128 rows of A
 // and half of B's 256, for twice the MMA work of a one-CTA 128 x 128 tile's loads.  Either way a
@@ -27,8 +28,7 @@
 // The backward pass's two products run as one launch, the one with the longer K first, dealt
 // so that the workers left over by its last round take more of the other (LinDeal).
 // The two single-thread roles branch once per item to code of its majors: with majors as run-time
-// values the MMA loop's descriptors left the uniform registers, and 8192 x 4096 -> 14336 took 711
-// instead of 627 us.
+// values in the MMA loop 8192 x 4096 -> 14336 took 711 instead of 658 us.
 //
 // Order.  Tiles run in bands of kBandRows tile rows, column by column inside a band, so the
 // tiles that are in flight together share few operand rows and columns in L2.
@@ -36,9 +36,15 @@
 // Accuracy.  The tensor core's accumulation truncates: a sum over K terms of random sign is off by
 // 1e-6 of its size for every 1024 of K, where fp32 with rounding stays below 1e-6.  Results of
 // 16 bits accumulate the whole K.  An fp32 dW, and a forward product whose z is kept in 8 bits
-// (where a sum's error decides which way a value rounds), accumulate 12 and 16 k-blocks in tensor
-// memory at a time, and the epilogue adds those sums in fp32 registers, rounded to nearest: 7e-7
-// and 1e-6 for any K.  Reading an accumulator holds the MMAs up for 0.4 us, 6 % at 16 blocks.
+// (where a sum's error decides which way a value rounds), accumulate kFold k-blocks in tensor
+// memory at a time, and the epilogue adds those sums in fp32 registers, rounded to nearest: dW is
+// off by 7e-7 for any K.  Values that round the other way than the exact z's put a kept z off by
+// (relative, 2048 x K -> 2048, mean of six; fp32 with rounding last)
+//     K = 1024: 1.4e-4, 1.1e-4, 1.0e-4 with 16, 12, 8 blocks; 0.6e-4
+//     K = 4096: 1.5e-4, 1.3e-4, 1.0e-4;                      1.1e-4
+// where the 8-bit steps themselves make about 1e-2; 8192 x 4096 -> 14336 with SiLU took 757, 807
+// and 849 us.  12 is within 1.3 times fp32's at 4096.  The short K stay behind it (1.85 times at
+// 1024), where a read costs the largest share.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -50,7 +56,7 @@ namespace mao {
 static __device__ DevStatus g_layer_status;
 
 constexpr int kBandRows = 8;
-constexpr int kFoldGrad = 12, kFoldKept = 16;
+constexpr int kFold = 12;  // k-blocks that an exact sum spends in tensor memory
 
 // Epilogues of the backward kernel; the forward kernel has its own (bias, activation,
 // residual, checkpoint of z).
@@ -316,9 +322,8 @@ struct LinCfg {
   static constexpr int A_TILE = 128 * 128;  // bytes: 128 rows of 64 elements per CTA
   static constexpr int B_TILE = 128 * 128;  // PAIR: half of B's rows per CTA
   static constexpr int STAGE_BYTES = A_TILE + B_TILE;
-  // As deep as shared memory allows: a stage comes back about 2.3 us after it was asked for (MMAs
-  // done, the commit seen, the load issued, L2, the barrier seen), so the bytes in flight set the
-  // pace of products that the power limit does not (4096^3: 118 us with 6 stages, 108 with 7).
+  // As deep as shared memory allows: the bytes in flight set the pace of products that the power
+  // limit does not (4096^3: 118 us with 6 stages, 108 with 7).
   static constexpr int STAGES = (224 * 1024) / STAGE_BYTES;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARPS = 16;
@@ -490,8 +495,7 @@ __device__ __forceinline__ void lin_body(const LinParams<FORWARD ? 1 : 2>& param
             mbar_arrive_expect_tx(&full_bar[s], Cfg::STAGE_BYTES);
           }
           lin_load<PAIR, A_MN>(st, &p.mapA, &full_bar[s], lead, kb * BK, t.m0 + 128 * (int)rank);
-          lin_load<PAIR, B_MN>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK,
-                                        t.n0 + 128 * (int)rank);
+          lin_load<PAIR, B_MN>(st + Cfg::A_TILE, &p.mapB, &full_bar[s], lead, kb * BK, t.n0 + 128 * (int)rank);
           if (++s == STAGES) s = 0, ph ^= 1;
         }
       };
