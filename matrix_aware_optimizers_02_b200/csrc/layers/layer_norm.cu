@@ -377,9 +377,11 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
           if constexpr (D > 0) Slot8<T>::get(x_slot(stage, i), B * 16).get(h[i]);
           else load_vec(x + i * G * 8, in[i]).get(h[i]);
         }
+        // behind the last column (0 - mean) rstd could overflow, and dy = 0 times that be NaN
+        const float rstd = in[i] ? now.rstd : 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          h[i][j] = mul2(add2(h[i][j], dup2(-now.mean)), dup2(now.rstd));
+          h[i][j] = mul2(add2(h[i][j], dup2(-now.mean)), dup2(rstd));
           dw[i][j] = fma2(u[i][j], h[i][j], dw[i][j]);
           db[i][j] = add2(db[i][j], u[i][j]);
           u[i][j] = mul2(u[i][j], w[i][j]);

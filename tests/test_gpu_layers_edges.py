@@ -320,3 +320,26 @@ def test_activations_far_out(api, act):
     R.close(db, s[0], 4e-6 * (1 + zd[0].abs()) * tail[0] + 2 * R.F32 * s[0].abs() + flush[0], "slope")
     R.close(dx, s, 1.01 * R.HALF_STEP[t] * s.abs() + 4e-6 * (1 + zd.abs()), "dx")
     assert math.isfinite(float(dx.float().abs().max()))
+
+
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("cols", [24, 264, 1032])
+def test_norm_backward_of_a_huge_constant_row(api, cols, kept):
+    """mean * rstd overflows, x - mean does not: lanes behind the last column must add nothing.
+
+    h = 0, so dx = rstd (u - mean u) with u = dy w.  Sums of cols terms of size 1 in fp32 are off
+    by cols 2^-24 at most, and dx is rounded to bf16 (2^-8 of its size)."""
+    g = torch.Generator("cuda").manual_seed(cols)
+    rows, rstd = 5, 316.0
+    x = torch.full((rows, cols), 2.0**122, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn(rows, cols, device="cuda", generator=g).bfloat16()
+    w = torch.randn(cols, device="cuda", generator=g)
+    mean = torch.full((rows,), 2.0**122, device="cuda")
+    dx, dw, db = api.layer_norm_backward(dy, api.checkpoint8(x) if kept else x, w, mean,
+                                         torch.full((rows,), rstd, device="cuda"))
+    u = dy.double() * w.double()
+    want = rstd * (u - u.mean(1, keepdim=True))
+    size = rstd * (u.abs() + u.abs().mean(1, keepdim=True))
+    assert ((dx.double() - want).abs() <= 2.0**-8 * want.abs() + (cols + 4) * 2.0**-23 * size).all()
+    assert (dw == 0).all()
+    assert ((db.double() - dy.double().sum(0)).abs() <= 8 * 2.0**-24 * dy.double().abs().sum(0)).all()
