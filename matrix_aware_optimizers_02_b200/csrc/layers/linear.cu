@@ -198,7 +198,8 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
     p.tiles_m = c.tiles_m, p.tiles_n = c.tiles_n;
     p.full = c.full, p.slices = c.slices;
     p.nk = c.nk, p.slice_blocks = c.slice_blocks;
-    p.fold = p.e.kind == LIN_GRAD32 || p.e.k.q != nullptr ? kFold : p.nk;
+    const bool kept = p.e.k.q != nullptr;
+    p.fold = kept || p.e.kind == LIN_GRAD32 ? fold_blocks(c.nk, kept) : c.nk;
     items += c.items();
     const Shape s = q[i].shape();
     flops += 2.0 * (double)s.M * (double)s.N * (double)s.K;

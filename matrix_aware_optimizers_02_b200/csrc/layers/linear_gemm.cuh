@@ -36,15 +36,9 @@
 // Accuracy.  The tensor core's accumulation truncates: a sum over K terms of random sign is off by
 // 1e-6 of its size for every 1024 of K, where fp32 with rounding stays below 1e-6.  Results of
 // 16 bits accumulate the whole K.  An fp32 dW, and a forward product whose z is kept in 8 bits
-// (where a sum's error decides which way a value rounds), accumulate kFold k-blocks in tensor
-// memory at a time, and the epilogue adds those sums in fp32 registers, rounded to nearest: dW is
-// off by 7e-7 for any K.  Values that round the other way than the exact z's put a kept z off by
-// (relative, 2048 x K -> 2048, mean of six; fp32 with rounding last)
-//     K = 1024: 1.4e-4, 1.1e-4, 1.0e-4 with 16, 12, 8 blocks; 0.6e-4
-//     K = 4096: 1.5e-4, 1.3e-4, 1.0e-4;                      1.1e-4
-// where the 8-bit steps themselves make about 1e-2; 8192 x 4096 -> 14336 with SiLU took 757, 807
-// and 849 us.  12 is within 1.3 times fp32's at 4096.  The short K stay behind it (1.85 times at
-// 1024), where a read costs the largest share.
+// (where a sum's error decides which way a value rounds), accumulate a few k-blocks in tensor
+// memory at a time (fold_blocks), and the epilogue adds those sums in fp32 registers, rounded to
+// nearest: dW is off by 7e-7 for any K.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -56,7 +50,23 @@ namespace mao {
 static __device__ DevStatus g_layer_status;
 
 constexpr int kBandRows = 8;
-constexpr int kFold = 12;  // k-blocks that an exact sum spends in tensor memory
+// k-blocks that a sum of nk of them spends in tensor memory at a time, in parts of one length
+// (16 as 8 + 8 take the time of 12 + 4).  At most 12 for an fp32 dW.  For a kept z the same, and
+// fewer for short K, where fp32's own error is smaller.  Error that values rounding the other way
+// than the exact z's put in a kept z, in fp32 sums' own (2048 x K -> 2048, mean of six seeds), and
+// the time of a product with SiLU and checkpoint, sustained:
+//     K          12 blocks         8                 6
+//     768   1.92   81 us     1.48   89 us     1.39   88 us    8192 x 768 -> 4096
+//     1024  1.85   98        1.65   98        1.35  109       8192 x 1024 -> 4096
+//     2048  1.44  295        1.19  318        1.01  350       8192 x 2048 -> 8192
+//     4096  1.18  938        0.94  989                        8192 x 4096 -> 14336 (16: 1.40, 876)
+// At 4096 parts of 11 give 1.11 in the time of 12.  K = 256 stays at 1.50 in one part.  The 8-bit
+// steps themselves are off a hundred times as far.  4 blocks at K = 1024: 1.12, 118 us.
+inline int fold_blocks(int nk, bool kept) {
+  const int most = !kept || nk > 32 ? 12 : (nk > 16 ? 8 : 6);
+  const int parts = (nk + most - 1) / most;
+  return (nk + parts - 1) / parts;
+}
 
 // Epilogues of the backward kernel; the forward kernel has its own (bias, activation,
 // residual, checkpoint of z).
