@@ -50,7 +50,9 @@ mao_status allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
 
 // Launch as a programmatic dependent of the kernel before it in the stream, which must be one
 // of this call's: launch latency and set-up overlap that kernel's end.  The kernel calls
-// wait_for_previous() before it touches global memory.
+// wait_for_previous() before it touches global memory, and takes what the kernel before wrote
+// by plain pointers: __restrict__ would say that nothing writes there while it runs, and allow
+// read-only loads that the wait does not order.
 template <class... P, class... A>
 mao_status launch_dependent(void (*kern)(P...), dim3 grid, int block, int smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t c = {};

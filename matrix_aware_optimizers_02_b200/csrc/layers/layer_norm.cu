@@ -470,9 +470,10 @@ __global__ void __launch_bounds__(kBlock<G>, BwdCfg<T, KEPT, RES, G, VPT>::kPerS
 // ------------------------------------------------------------------ column reduction
 // 32 columns per block, 32 warps over the parts, 4 loads in flight each; joined in a fixed
 // order, so the sums do not depend on how blocks are scheduled.  blockIdx.y picks one of two
-// sums whose parts lie one behind the other.
-__global__ void __launch_bounds__(1024) col_reduce_kernel(const float* __restrict__ part, int parts, int cols,
-                                                          float* __restrict__ out0, float* __restrict__ out1) {
+// sums whose parts lie one behind the other.  No __restrict__: the kernel before may still
+// write `part` when this one starts.
+__global__ void __launch_bounds__(1024) col_reduce_kernel(const float* part, int parts, int cols, float* out0,
+                                                          float* out1) {
   __shared__ float sh[32][33];
   wait_for_previous();
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;

@@ -1,0 +1,39 @@
+"""Rules of the trained layers that a machine without a GPU can check: in the kernels' source,
+in the host's plans, and in the binding."""
+
+import glob
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LAYERS = os.path.join(ROOT, "matrix_aware_optimizers_02_b200", "csrc", "layers")
+
+
+def _functions():
+    """(name, head, body) of each function of the trained layers' sources: head is all between
+    the end of what comes before and the body's opening brace."""
+    for path in sorted(glob.glob(os.path.join(LAYERS, "*.cu*"))):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for m in re.finditer(r"__(?:global|device)__[^;{}]*?\b(\w+)\s*\(((?:[^(){};]|\([^(){};]*\))*)\)\s*\{", text):
+            depth, i = 1, m.end()
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[i], 0)
+                i += 1
+            yield m.group(1), m.group(0), text[m.end():i]
+
+
+def test_dependent_kernels_promise_nothing_of_their_inputs():
+    """A kernel that waits for the one before it may run while that one still writes what this
+    one reads.  __restrict__ on such a pointer would promise the compiler that nobody does, and
+    allow loads that the wait does not order."""
+    functions = list(_functions())
+    waits = {n for n, _, body in functions if "wait_for_previous()" in body}
+    kernels = [(n, head, body) for n, head, body in functions
+               if "__global__" in head and (n in waits or any(re.search(rf"\b{w}\s*<", body) for w in waits))]
+    names = {n for n, _, _ in kernels}
+    assert {"col_reduce_kernel", "lin_join_kernel", "lin_kernel", "lin_pair_kernel"} <= names
+    for n, head, body in kernels:
+        assert "__restrict__" not in head, f"{n} takes a __restrict__ pointer"
+    for n, head, body in functions:
+        if n in waits:
+            assert "__ldg" not in body and "ld.global.nc" not in body, f"{n} reads by the non-coherent path"
