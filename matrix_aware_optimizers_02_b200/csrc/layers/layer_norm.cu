@@ -9,8 +9,13 @@
 // shared memory: up to 200 KB in flight per SM, where the same loads held in registers, one
 // row ahead, left the passes waiting (backward 8191 x 1536 with residual: 49 us).
 //
-// Mean and variance: two passes over the registers (sum of x, then of (x - mean)^2), so
-// a large mean costs no digits.
+// Mean and variance: two passes over the registers (sum of x, then of (x - m)^2).  m, a rounded
+// sum times a rounded reciprocal, is off by a few steps of itself, which a row far from zero
+// shows rstd-fold (a constant 10944 in 14336 columns: y off by 0.3).  Rows whose |m| is more than
+// kFar deviations therefore sum x - m as well: delta = mean(x - m) corrects the mean, the variance
+// (less delta^2) and y, and what is left of the error is a few steps of delta.  Nearer rows skip
+// that: m's error, a few 2^-24 of at most kFar deviations, is that of their other roundings
+// (16384 x 4096 bf16 with checkpoint: 67.6 us, far rows 76.7, without any of this 65.5).
 #include "layer_host.h"
 
 namespace mao {
@@ -80,6 +85,8 @@ __device__ __forceinline__ Vec8<T> load_vec(const T* p, bool ok) {
 }
 
 // ------------------------------------------------------------------ forward
+constexpr float kFar = 4.0f;
+
 struct FwdArgs {
   const void* x;
   const void* w;
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
   constexpr int D = Cfg::kStages;
   constexpr uint32_t kVec = Slot8<T>::kBytes * B;  // one vector of every thread
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ __align__(16) float sh[2][32];
+  __shared__ __align__(16) float sh[3][32];
   const uint32_t slot0 = smem_u32(ring) + threadIdx.x * 16;
   const int t = threadIdx.x % G;
   const int cols = a.cols;
@@ -147,16 +154,21 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) fetch(d);
   }
-  f2 w[VPT][4], b[VPT][4];
+  // the weight and the bias stay in registers, but for rows of 4 vectors a thread, where they would
+  // be spilled: those read them anew for each row (4096 x 20480 bf16: 121 us, held and spilled 182)
+  constexpr bool kHold = VPT < 4;
+  f2 w[kHold ? VPT : 1][4], b[kHold ? VPT : 1][4];
+  auto params = [&](int i, f2 (&wi)[4], f2 (&bi)[4]) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (i * G + t) * 8;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[i][j] = b[i][j] = dup2(0.0f);
-    if (c < cols) {
-      load_param8<T>(a.w, a.w_f32, c, w[i]);
-      if (a.b != nullptr) load_param8<T>(a.b, a.w_f32, c, b[i]);
+    for (int j = 0; j < 4; ++j) wi[j] = bi[j] = dup2(0.0f);
+    if (in[i]) {
+      load_param8<T>(a.w, a.w_f32, (i * G + t) * 8, wi);
+      if (a.b != nullptr) load_param8<T>(a.b, a.w_f32, (i * G + t) * 8, bi);
     }
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) params(i, w[i], b[i]);
   }
   uint32_t row = row0;
   int stage = 0;
@@ -184,12 +196,12 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
       for (int j = 0; j < 4; ++j) p = add2(p, v[i][j]);
     float s[1] = {p.x + p.y};
     row_sum<G, 1>(s, sh[0]);
-    const float mean = s[0] * a.inv_cols;
+    const float m = s[0] * a.inv_cols;
     p = dup2(0.0f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], dup2(-mean));
+      for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], dup2(-m));
       if (in[i]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) p = fma2(v[i][j], v[i][j], p);
@@ -197,7 +209,30 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
     }
     s[0] = p.x + p.y;
     row_sum<G, 1>(s, sh[1]);
-    const float rstd = rsqrtf(s[0] * a.inv_cols + a.eps);  // off by at most 2 steps
+    float var = s[0] * a.inv_cols, mean = m;
+    // all threads of a row hold the same sums; a block of two rows has barriers that both take part in
+    const bool far = m * m > kFar * kFar * (var + a.eps);
+    if ((R > 1 && G > 32) ? __syncthreads_or(far) : far) {
+      f2 d = dup2(0.0f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (in[i]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d = add2(d, v[i][j]);
+        }
+      s[0] = d.x + d.y;
+      row_sum<G, 1>(s, sh[2]);
+      if (far) {
+        const float delta = s[0] * a.inv_cols;
+        mean += delta;
+        var = fmaxf(fmaf(-delta, delta, var), 0.0f);  // not NaN here: far rows compare
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], dup2(-delta));
+      }
+    }
+    const float rstd = rsqrtf(var + a.eps);  // off by at most 2 steps
     if (live && t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
@@ -205,8 +240,10 @@ __global__ void __launch_bounds__(kBlock<G>, FwdCfg<T, G, VPT>::kPerSm) norm_ker
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       f2 o[4];
+      if constexpr (!kHold) params(i, w[0], b[0]);
+      constexpr int kStep = kHold ? 1 : 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], dup2(rstd)), w[i][j], b[i][j]);
+      for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], dup2(rstd)), w[i * kStep][j], b[i * kStep][j]);
       Vec8<T> q;
       q.set(o);
       if (live && in[i]) q.store(y + i * G * 8);
