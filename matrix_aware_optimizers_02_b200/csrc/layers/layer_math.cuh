@@ -307,23 +307,45 @@ __device__ __forceinline__ f2 relu2v(f2 z) {  // a NaN stays one
   return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
 }
 
-// EXACT: fp32 results (erff); otherwise results that are rounded to 16 bits.
+// For fp32 results, each value to a few steps of itself in the tails too: no 1 + erf or 1 + tanh,
+// which cancel where z << 0, and no flushed or approximate exponential.
+//   sigmoid(v) = (v < 0 ? t : 1) / (1 + t),  t = exp(-|v|)
+//   Phi(-a) = erfc(a / sqrt 2) / 2 = exp(-a^2 / 2) erfcx(a / sqrt 2) / 2, where z^2 is exact for the 8 bits of
+//   a checkpoint's value and erfcx falls off like 1 / a, so that no rounding counts a^2 times
+// Bound by these instructions: 16384 x 4096 read back to fp32 takes 61 us without an activation, 88 with
+// silu, 96 with gelu_tanh, 158 with gelu (87 with 1 + erff, which is off by 4e-2 of the value at z = -5).
+// A rounded reciprocal in place of the quotient took the same.
+__device__ __forceinline__ float sigmoid32(float v) {
+  const float t = expf(-fabsf(v));
+  return (v < 0.0f ? t : 1.0f) / (1.0f + t);
+}
+template <int ACT>
+__device__ __forceinline__ float act_value32(float z) {
+  if constexpr (ACT == MAO_ACT_GELU) {
+    const float a = fabsf(z);
+    const float tail = 0.5f * expf(-0.5f * z * z) * erfcxf(a * 0.7071067811865476f);
+    return z * (z < 0.0f ? tail : 1.0f - tail);
+  } else if constexpr (ACT == MAO_ACT_GELU_TANH) {
+    return z * sigmoid32(z * fmaf(z * z, 2.0f * kGeluA * kGeluB, 2.0f * kGeluA));
+  } else {
+    return z * sigmoid32(z);  // silu
+  }
+}
+
+// EXACT: fp32 results; otherwise results that are rounded to 16 bits.
 template <int ACT, bool EXACT = false>
 __device__ __forceinline__ f2 act_value(f2 z) {
-  if constexpr (ACT == MAO_ACT_RELU) {
+  if constexpr (EXACT && (ACT == MAO_ACT_GELU || ACT == MAO_ACT_GELU_TANH || ACT == MAO_ACT_SILU)) {
+    return make_float2(act_value32<ACT>(z.x), act_value32<ACT>(z.y));
+  } else if constexpr (ACT == MAO_ACT_RELU) {
     return relu2v(z);
   } else if constexpr (ACT == MAO_ACT_RELU2) {
     const f2 r = relu2v(z);
     return mul2(r, r);
   } else if constexpr (ACT == MAO_ACT_GELU) {
-    if constexpr (EXACT) {
-      const f2 h = mul2(z, dup2(0.5f));
-      return mul2(h, make_float2(1.0f + erff(z.x * 0.7071067811865476f), 1.0f + erff(z.y * 0.7071067811865476f)));
-    } else {
-      f2 c, d;
-      normal_cdf(z, c, d);
-      return mul2(z, c);
-    }
+    f2 c, d;
+    normal_cdf(z, c, d);
+    return mul2(z, c);
   } else if constexpr (ACT == MAO_ACT_GELU_TANH) {
     return mul2(z, inv_1p_exp2(gelu_tanh_arg(z, mul2(z, z))));
   } else if constexpr (ACT == MAO_ACT_SILU) {

@@ -1,6 +1,8 @@
 """The trained-layer operators where an evaluation loses digits.  F32 is half a step of fp32, TC a
 whole one (an add that truncates)."""
 
+import math
+
 import pytest
 import torch
 
@@ -62,3 +64,44 @@ def test_norm_far_from_zero(api, cols, dt):
     tol = 1.01 * R.HALF_STEP[t] * want.abs() + scaled * (rel[:, None] + 8 * R.F32)
     tol = tol + (far * rstd_w)[:, None] * w.double().abs() + 4 * R.F32 * (scaled + b.double().abs())
     R.close(y, want, tol, "y")
+
+
+# ------------------------------------------------------------------ fp32 read-back through an activation
+@pytest.mark.parametrize("act", R.ACTS)
+def test_restore_to_fp32_keeps_the_tails(api, act):
+    """Relative to each value, from -108 to 108 (where exp(-|z|) and the results are subnormal)
+    and far outside.  In half steps: CUDA's expf is off by at most 2 units in the last place (4
+    half steps), erfcf-like functions by 4 (8); a relative error of an exponential's argument v
+    counts |v| times; every product, quotient and sum of one sign adds 1.
+
+    gelu: 4 + 8, the tail function's argument 2 (its own relative slope is at most 1), products 3,
+    and where z > 0 one from 1 - tail: 18.  silu: 4, the sum 2, quotient and products 3: 9.
+    gelu_tanh: the same with an argument off by 4, so 4 |v| more.  A subnormal exponential is off
+    by 2^-150, its result by |z| times that, and rounds to 2^-150 itself."""
+    z = torch.cat([torch.linspace(-14, 14, 16384), torch.linspace(-108, 108, 8192),
+                   torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-6, -1e-6, 1e15, -1e15, 1e25, -1e25, 1e38, -1e38] * 2 + [0.0] * 8)])
+    z = z.view(-1, 32).cuda()
+    k = api.checkpoint8(z)
+    z = k.restore()
+    assert torch.equal(z.double(), R.unpack(k.q, k.e, 32))
+    zd = z.double()
+    tiny = torch.zeros_like(zd)
+    if act == "gelu":
+        half = torch.full_like(zd, 18.0)
+    elif act == "silu":
+        half = torch.full_like(zd, 10.0)
+    elif act == "gelu_tanh":
+        v = 2 * math.sqrt(2 / math.pi) * (zd.abs() + 0.044715 * zd.abs() ** 3)
+        half = 10 + 4 * v.clamp(max=120.0)
+    else:
+        half = torch.full_like(zd, 1.0)
+    if act in ("gelu", "silu", "gelu_tanh"):
+        tiny = 2.0 ** -149 * (1 + zd.abs().clamp(max=128.0))
+    # the 64-bit values of the tails, without the cancellation of 1 + tanh
+    want = R.act(zd, act) if act != "gelu_tanh" else \
+        zd * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (zd + 0.044715 * zd ** 3))
+    want = torch.where(want > torch.finfo(torch.float32).max, torch.full_like(want, math.inf), want)
+    R.close(k.restore(act=act), want, 1.01 * half * R.F32 * want.abs() + tiny, act)
+    nan = api.Checkpoint8(torch.zeros((1, 32), dtype=torch.int8, device="cuda"),
+                          torch.full((1, 1), 255, dtype=torch.uint8, device="cuda"), 32, torch.float32)
+    assert torch.isnan(nan.restore(act=act)).all()
