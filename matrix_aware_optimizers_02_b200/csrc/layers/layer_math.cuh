@@ -370,7 +370,9 @@ __device__ __forceinline__ f2 act_slope(f2 z) {
     // d/dz z s(v(z)) with v = 2 sqrt(2/pi) (z + b z^3): s + z s (1 - s) v'
     const f2 z2 = mul2(z, z);
     const f2 s = inv_1p_exp2(gelu_tanh_arg(z, z2));
-    const f2 dv = fma2(z2, dup2(6.0f * kGeluA * kGeluB), dup2(2.0f * kGeluA));
+    // z^2 held finite: where it is not, z s (1 - s) is 0, and 0 times an infinite v' would be NaN
+    const f2 zz = make_float2(fminf(z2.x, 1e30f), fminf(z2.y, 1e30f));
+    const f2 dv = fma2(zz, dup2(6.0f * kGeluA * kGeluB), dup2(2.0f * kGeluA));
     const f2 sp = fma2(mul2(s, s), dup2(-1.0f), s);
     return fma2(mul2(z, sp), dv, s);
   } else if constexpr (ACT == MAO_ACT_SILU) {

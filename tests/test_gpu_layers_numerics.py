@@ -105,3 +105,30 @@ def test_restore_to_fp32_keeps_the_tails(api, act):
     nan = api.Checkpoint8(torch.zeros((1, 32), dtype=torch.int8, device="cuda"),
                           torch.full((1, 1), 255, dtype=torch.uint8, device="cuda"), 32, torch.float32)
     assert torch.isnan(nan.restore(act=act)).all()
+
+
+# ------------------------------------------------------------------ slopes of the largest values
+@pytest.mark.parametrize("act", [a for a in R.ACTS if a != "none"])
+def test_slopes_of_the_largest_values(api, act):
+    """z up to the end of bf16's range, whose square fp32 cannot hold: the slope is 0, 1 or 2 z."""
+    t = torch.bfloat16
+    z = torch.tensor([1e4, 1e9, 1e13, 1.8e19, 2e19, 1e25, 1e30, 1.6e38], device="cuda").to(t)
+    z = torch.cat([z, -z, z, -z]).view(1, 32)
+    dy = torch.ones((1, 32), dtype=t, device="cuda")
+    w = torch.eye(32, dtype=t, device="cuda")
+    want = torch.where(z.double() > 0, 2 * z.double() if act == "relu2" else torch.ones_like(z.double()), 0.0)
+    for zz in (z, api.checkpoint8(z.view(32, 1).expand(32, 32).contiguous())):
+        rows = 1 if zz is z else 32
+        d = dy.expand(rows, 32).contiguous()
+        x = torch.zeros((rows, 32), dtype=t, device="cuda")
+        s = want if rows == 1 else want.view(32, 1).expand(32, 32)
+        if rows == 32 and act == "relu2":
+            v = zz.restore().double()
+            s = torch.where(v > 0, 2 * v, 0.0)
+        dx, dw, db = api.linear_backward(d, x, w, z=zz, act=act)
+        R.close(dx, s, 1.01 * R.HALF_STEP[t] * s.abs() + 1e-6, "dx")
+        assert (dw == 0).all()
+        # fp32 sums of at most 32 terms; two of relu2's largest pass fp32's end
+        total = s.sum(0)
+        total = torch.where(total > torch.finfo(torch.float32).max, torch.full_like(total, math.inf), total)
+        R.close(db, total, 34 * R.F32 * s.abs().sum(0) + 1e-6, "db")
