@@ -199,7 +199,7 @@ mao_status products(const Product* q, int n, const LinPlans& plans, const LinCol
     p.full = c.full, p.slices = c.slices;
     p.nk = c.nk, p.slice_blocks = c.slice_blocks;
     const bool kept = p.e.k.q != nullptr;
-    p.fold = kept || p.e.kind == LIN_GRAD32 ? fold_blocks(c.nk, kept) : c.nk;
+    p.fold = kept || p.e.kind == LIN_GRAD32 ? fold_blocks(c.nk, kept) : equal_parts(c.nk, kLongFold);
     items += c.items();
     const Shape s = q[i].shape();
     flops += 2.0 * (double)s.M * (double)s.N * (double)s.K;

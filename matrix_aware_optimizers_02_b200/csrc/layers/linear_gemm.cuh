@@ -34,11 +34,12 @@
 // tiles that are in flight together share few operand rows and columns in L2.
 //
 // Accuracy.  The tensor core's accumulation truncates: a sum over K terms of random sign is off by
-// 1e-6 of its size for every 1024 of K, where fp32 with rounding stays below 1e-6.  Results of
-// 16 bits accumulate the whole K.  An fp32 dW, and a forward product whose z is kept in 8 bits
-// (where a sum's error decides which way a value rounds), accumulate a few k-blocks in tensor
-// memory at a time (fold_blocks), and the epilogue adds those sums in fp32 registers, rounded to
-// nearest: dW is off by 7e-7 for any K.
+// 1e-6 of its size for every 1024 of K, where fp32 with rounding stays below 1e-6, and one of terms
+// of one sign by up to 7e-6.  So the sums leave tensor memory after a number of k-blocks, and the
+// epilogue adds them in fp32 registers, rounded to nearest: after a few for an fp32 dW and for a
+// forward product whose z is kept in 8 bits (where a sum's error decides which way a value rounds),
+// after 128 for other results of 16 bits.  dW in fp32 is then off by 4.7e-7 (1024 tokens) to 7.7e-7
+// (131072) of its size in the mean square for terms of random sign, by 6.4e-7 at most for one sign.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -62,11 +63,15 @@ constexpr int kBandRows = 8;
 //     4096  1.18  938        0.94  989                        8192 x 4096 -> 14336 (16: 1.40, 876)
 // At 4096 parts of 11 give 1.11 in the time of 12.  K = 256 stays at 1.50 in one part.  The 8-bit
 // steps themselves are off a hundred times as far.  4 blocks at K = 1024: 1.12, 118 us.
-inline int fold_blocks(int nk, bool kept) {
-  const int most = !kept || nk > 32 ? 12 : (nk > 16 ? 8 : 6);
+// Other 16-bit results: 128 (8192 terms).  Terms of one sign lose about a step of the result per
+// truncated add: 8.7e-4 of it after 131072 in one part, where fp16's half step is 4.9e-4; 8192
+// lose 6e-5.  K up to 8192 stays in one part.
+inline int equal_parts(int nk, int most) {
   const int parts = (nk + most - 1) / most;
   return (nk + parts - 1) / parts;
 }
+inline int fold_blocks(int nk, bool kept) { return equal_parts(nk, !kept || nk > 32 ? 12 : (nk > 16 ? 8 : 6)); }
+constexpr int kLongFold = 128;
 
 // Epilogues of the backward kernel; the forward kernel has its own (bias, activation,
 // residual, checkpoint of z).

@@ -132,3 +132,26 @@ def test_slopes_of_the_largest_values(api, act):
         total = s.sum(0)
         total = torch.where(total > torch.finfo(torch.float32).max, torch.full_like(total, math.inf), total)
         R.close(db, total, 34 * R.F32 * s.abs().sum(0) + 1e-6, "db")
+
+
+# ------------------------------------------------------------------ long sums
+def _positive(g, rows, cols, lo, hi, t):
+    return torch.empty((rows, cols), device="cuda").uniform_(lo, hi, generator=g).to(t)
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_16_bit_results_of_long_one_signed_sums(api, dt):
+    """2^17 tokens into a 16-bit dW.  With sums joined in fp32 every 8192 terms a sum is off by 512
+    truncated adds of at most a step each (and 40 for the products inside and the joining), beside
+    half a step of the result."""
+    g = _gen(3)
+    t = DT[dt]
+    rows, n, m = 1 << 17, 4096, 4096
+    dy, x = _positive(g, rows, m, 0.05, 0.15, t), _positive(g, rows, n, 0.05, 0.15, t)
+    w = torch.zeros((m, n), dtype=t, device="cuda")
+    _, dw, _ = api.linear_backward(dy, x, w, need_dx=False, need_db=False, dw_dtype=t)
+    del w
+    want = torch.zeros((m, 256), dtype=torch.float64, device="cuda")
+    for r in range(0, rows, 16384):
+        want += dy[r:r + 16384].double().t() @ x[r:r + 16384, :256].double()
+    R.close(dw[:, :256], want, (1.01 * R.HALF_STEP[t] + 552 * R.TC) * want, "dw")
