@@ -121,6 +121,8 @@ class Checkpoint8:
         if q.dim() != 2 or e.dim() != 2 or q.shape[1] != 32 * blocks or tuple(e.shape) != (q.shape[0], blocks):
             raise ValueError(f"a checkpoint of {cols} columns has q (rows, {32 * blocks}) and e (rows, {blocks}), got "
                              f"{tuple(q.shape)} and {tuple(e.shape)}")
+        if max(q.shape[0], cols) > _MOST:
+            raise ValueError(f"a checkpoint of {q.shape[0]} x {cols}: at most {_MOST} rows and columns")
         if not q.is_contiguous() or not e.is_contiguous():
             raise ValueError("q and e must be contiguous")
         self.q, self.e, self.cols, self.dtype = q, e, cols, dtype
@@ -266,6 +268,8 @@ def _check_weight(W: torch.Tensor, device, dtype) -> Tuple[int, int]:
         raise ValueError("W must be 2-D (out features, in features) and contiguous")
     if W.shape[0] % 8 or W.shape[1] % 8 or W.numel() == 0:
         raise ValueError(f"W has shape {tuple(W.shape)}: both sides must be positive multiples of 8")
+    if max(W.shape) > _MOST:
+        raise ValueError(f"W has shape {tuple(W.shape)}: at most {_MOST} rows and columns")
     return W.shape
 
 

@@ -5,6 +5,11 @@ import glob
 import os
 import re
 
+import pytest
+import torch
+
+from matrix_aware_optimizers_02_b200 import layers
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 LAYERS = os.path.join(ROOT, "matrix_aware_optimizers_02_b200", "csrc", "layers")
 
@@ -37,3 +42,23 @@ def test_dependent_kernels_promise_nothing_of_their_inputs():
     for n, head, body in functions:
         if n in waits:
             assert "__ldg" not in body and "ld.global.nc" not in body, f"{n} reads by the non-coherent path"
+
+
+@pytest.mark.parametrize("big", [2**30 + 8, 2**32 + 8])
+def test_weights_and_checkpoints_past_the_limit_are_refused(monkeypatch, big):
+    """The C structs' fields have 32 bits: 2^32 + 8 rows of a weight, or columns of a checkpoint,
+    would reach the library as 8 without an error."""
+    monkeypatch.setattr(layers, "_check", lambda *a, **k: None)
+    t = torch.bfloat16
+
+    def meta(rows, cols, dtype=t):
+        return torch.empty((rows, cols), dtype=dtype, device="meta")
+
+    calls = [lambda: layers.linear(meta(1, 8), meta(big, 8)), lambda: layers.linear(meta(1, big), meta(8, big)),
+             lambda: layers.linear_backward(meta(1, big), meta(1, 8), meta(big, 8))]
+    blocks = (big + 31) // 32
+    calls += [lambda: layers.Checkpoint8(meta(1, 32 * blocks, torch.int8), meta(1, blocks, torch.uint8), big, t),
+              lambda: layers.Checkpoint8(meta(big, 32, torch.int8), meta(big, 1, torch.uint8), 8, t)]
+    for call in calls:
+        with pytest.raises(ValueError, match="at most"):
+            call()
