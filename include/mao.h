@@ -458,7 +458,9 @@ MAO_API mao_status mao_linear(const mao_linear_args* a, void* workspace, size_t 
  *   dz = dy act'(z),   dx = dz W,   dW (+)= dz^T x,   db = sum over rows of dz.
  * dz is rounded to the activations' type before the two products (their tensor-core
  * operands have that type); db sums the unrounded values.  x and z are read from tensors or,
- * where those are NULL, from their checkpoints; z is not read for MAO_ACT_NONE.  dW is fp32
+ * where those are NULL, from their checkpoints; z is not read for MAO_ACT_NONE.  A checkpoint
+ * of x is read back in `dtype`: exactly in bf16, and in fp16 where it was made from fp16 (other
+ * values above 65504 become infinite); one of z is read in fp32.  dW is fp32
  * or of the activations' type, m x n with rows contiguous; `accumulate` adds to an fp32 dW
  * what this call computes.  dx, dW and db may each be NULL.
  */

@@ -103,7 +103,8 @@ class Checkpoint8:
 
     q: int8 (rows, 32 * ceil(cols / 32)); e: uint8 (rows, ceil(cols / 32)); a value is
     q * 2^(e - 127) (include/mao.h, mao_ckpt8, has the format in full).  `dtype` is the type
-    that restore() gives back by default and the one the backward passes work in.
+    of the values it was made from, which restore() gives back by default.  Every value is exact
+    in bfloat16 and float32; float16 holds those of a float16 checkpoint.
     A checkpoint takes 33/64 of the bytes of a 16-bit matrix.
     """
 
@@ -325,7 +326,7 @@ def linear_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8], W: to
                     need_db: bool = True):
     """The linear layer's gradient: (dx, dw, db); the residual's own gradient is dy.
 
-    x is the forward input or its Checkpoint8; z, which act other than "none" needs, is what
+    x is the forward input or its Checkpoint8 (of float16 values where dy is float16); z, which act other than "none" needs, is what
     linear() kept.  dw (m, n) is float32 or of dy's type: the given tensor (a batch's G), or a
     new one of dw_dtype.  accumulate adds to the given float32 dw.  db is float32.  What
     need_* leaves out comes back as None and costs nothing.
@@ -340,6 +341,9 @@ def linear_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8], W: to
     if dy.shape[1] != m:
         raise ValueError(f"dy has {dy.shape[1]} columns, W gives {m}")
     xp, ld_x, xc = _check_kept("x", x, (rows, n), dev, dt)
+    if need_dw and dt == torch.float16 and isinstance(x, Checkpoint8) and x.dtype != dt:
+        raise TypeError(f"x is a checkpoint of {x.dtype} values, which the product dz^T x would read as {dt}: above "
+                        f"65504 they would be infinite")
     zp, ld_z, zc = None, 0, _NO_CKPT
     if a_id:
         if z is None:

@@ -62,3 +62,17 @@ def test_weights_and_checkpoints_past_the_limit_are_refused(monkeypatch, big):
     for call in calls:
         with pytest.raises(ValueError, match="at most"):
             call()
+
+
+@pytest.mark.parametrize("kept", [torch.bfloat16, torch.float32])
+def test_float16_products_refuse_checkpoints_of_wider_types(monkeypatch, kept):
+    """dW = dz^T x reads x back in dy's type, and float16 ends at 65504."""
+    monkeypatch.setattr(layers, "_check", lambda *a, **k: None)
+    k = object.__new__(layers.Checkpoint8)
+    k.q = torch.empty((4, 32), dtype=torch.int8, device="meta")
+    k.e = torch.empty((4, 1), dtype=torch.uint8, device="meta")
+    k.cols, k.dtype = 16, kept
+    dy = torch.empty((4, 8), dtype=torch.float16, device="meta")
+    w = torch.empty((8, 16), dtype=torch.float16, device="meta")
+    with pytest.raises(TypeError, match="checkpoint of"):
+        layers.linear_backward(dy, k, w)
