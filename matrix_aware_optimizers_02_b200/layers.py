@@ -2,19 +2,20 @@
 backward passes, and 8-bit checkpoints of activations that the backward passes read.
 
     from matrix_aware_optimizers_02_b200 import api
-    h, mean, rstd, hk, = api.layer_norm(x, w, b, checkpoint=True)      # hk: h in 8 bits
+    h, mean, rstd, hk = api.layer_norm(x, w, b, checkpoint=True)      # hk: h in 8 bits
     a, zk = api.linear(h, W.bfloat16(), bias, act="gelu", checkpoint=True)
     ...
     dh, _, dbias = api.linear_backward(da, hk, W.bfloat16(), z=zk, act="gelu", dw=G)
     dx, dw, db = api.layer_norm_backward(dh, x, w, mean, rstd, dres=dy)
     muon()            # a MuonBatch built on (W, G, M)
 
-Explicit forward / backward pairs: no autograd graph is recorded, and a tensor that
-requires grad is refused while grad mode is on.  Activations are 2-D CUDA tensors (a row
-per token) with contiguous rows of a multiple of 8 elements, 16-byte aligned; a row stride
-larger than the row is allowed.  Work runs on the current stream of the tensors' device.
-Outputs and scratch come from torch's allocator on that stream; nothing is kept between
-calls.  Argument marshalling only; every arithmetic step runs in the library's kernels.
+Explicit forward / backward pairs: no autograd graph is recorded.  A tensor that requires
+grad is refused while grad mode is on, one with a forward-mode tangent always.
+Activations are 2-D CUDA tensors (a row per token) with contiguous rows of a multiple of 8
+elements, 16-byte aligned; a row stride larger than the row is allowed.  Work runs on the
+current stream of the tensors' device.  Outputs and scratch come from torch's allocator on
+that stream; nothing is kept between calls.  Argument marshalling only; every arithmetic
+step runs in the library's kernels.
 """
 
 from __future__ import annotations
@@ -23,6 +24,7 @@ import ctypes
 from typing import Optional, Tuple, Union
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L
 
@@ -30,6 +32,12 @@ _DTYPES = {torch.float32: L.MAO_F32, torch.bfloat16: L.MAO_BF16, torch.float16: 
 _HALF = (torch.bfloat16, torch.float16)
 _MOST = 2**30
 _NO_CKPT = L.Ckpt8(None, None, 0, 0)
+
+
+def _has_tangent(t: torch.Tensor) -> bool:
+    # outside a dual level, which is nearly always, one comparison; no_grad leaves forward mode on
+    return (getattr(forward_ad, "_current_level", 0) >= 0 and torch._C._is_fwd_grad_enabled() and
+            forward_ad.unpack_dual(t).tangent is not None)
 
 
 def _check(name: str, t: torch.Tensor, device=None, dtype=None) -> None:
@@ -43,6 +51,8 @@ def _check(name: str, t: torch.Tensor, device=None, dtype=None) -> None:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: these calls record no graph (use torch.no_grad() or detach())")
+    if _has_tangent(t):
+        raise ValueError(f"{name} carries a forward-mode tangent: these calls have none (use unpack_dual(...).primal)")
 
 
 def _check_acts(name: str, t: torch.Tensor, shape=None, device=None, dtype=None) -> int:

@@ -76,3 +76,31 @@ def test_float16_products_refuse_checkpoints_of_wider_types(monkeypatch, kept):
     w = torch.empty((8, 16), dtype=torch.float16, device="meta")
     with pytest.raises(TypeError, match="checkpoint of"):
         layers.linear_backward(dy, k, w)
+
+
+def test_forward_mode_tangents_are_refused():
+    """These calls record no graph, so a tangent would be dropped without an error; under no_grad
+    too, which does not stop forward mode."""
+    import torch.autograd.forward_ad as fw
+
+    class OnDevice(torch.Tensor):  # passes for a CUDA tensor, so that the check goes on
+        is_cuda = True
+
+    x = torch.zeros((4, 8))
+    plain = torch.Tensor._make_subclass(OnDevice, x)
+    layers._check("x", plain)
+    with fw.dual_level():
+        d = fw.make_dual(x, torch.ones_like(x))
+        on = torch.Tensor._make_subclass(OnDevice, x)
+        dual = fw.make_dual(on, torch.ones_like(x))
+        if not isinstance(dual, OnDevice):
+            dual = dual.as_subclass(OnDevice)
+        assert fw.unpack_dual(dual).tangent is not None and fw.unpack_dual(d).tangent is not None
+        layers._check("x", plain)
+        for mode in (torch.enable_grad, torch.no_grad):
+            with mode(), pytest.raises(ValueError, match="tangent"):
+                layers._check("x", dual)
+        layers._check("x", fw.unpack_dual(dual).primal)
+        with fw._set_fwd_grad_enabled(False):
+            layers._check("x", dual)
+    layers._check("x", plain)
