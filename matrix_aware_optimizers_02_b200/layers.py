@@ -99,9 +99,13 @@ def _elsewhere(device) -> bool:
     return device.index != torch.cuda.current_device()
 
 
-# torch.cuda.current_stream(device).cuda_stream without building a Stream object: 0.1 against
-# 2.2 us, of a call that takes about 10
-_stream = torch._C._cuda_getCurrentRawStream
+def _stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same without building a Stream object: 0.1 against 2.2 us, of a call that takes about 10
+# (a torch built without CUDA does not have it, and imports all the same)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -4,6 +4,8 @@ in the host's plans, and in the binding."""
 import glob
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -104,3 +106,26 @@ def test_forward_mode_tangents_are_refused():
         with fw._set_fwd_grad_enabled(False):
             layers._check("x", dual)
     layers._check("x", plain)
+
+
+_WITHOUT_CUDA = """
+import torch
+for name in ("_cuda_getCurrentRawStream",):  # a torch built without CUDA has no such name
+    delattr(torch._C, name)
+from matrix_aware_optimizers_02_b200 import api, layers
+class Stream:
+    cuda_stream = 77
+torch.cuda.current_stream = lambda device: Stream if device == 3 else None
+assert layers._stream(3) == 77
+try:
+    api.checkpoint8(torch.zeros((4, 16)))
+except ValueError as e:
+    assert "CUDA tensor" in str(e)
+print("imported")
+"""
+
+
+def test_binding_imports_without_cuda_in_torch():
+    """The package's host side (layer sets, plans, refusals) works with a torch built for the CPU."""
+    r = subprocess.run([sys.executable, "-c", _WITHOUT_CUDA], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "imported" in r.stdout, r.stdout + r.stderr
