@@ -1,7 +1,8 @@
 /*
  * mao_testing.h — entry points of libmao that exist for verification: they
  * expose the grouped tensor-core GEMM core on its own so that tests can check
- * it against a plain fp32 matrix product, independently of any optimizer.
+ * it against a plain fp32 matrix product, independently of any optimizer, and
+ * what the trained layers hold on the host (the dealing of work, the status).
  * Same conventions as mao.h (caller-owned device buffers, 16-byte alignment,
  * validation before any launch, no synchronisation).
  */
@@ -75,6 +76,21 @@ MAO_API mao_status mao_test_set_table_kernel(int32_t policy);
  * aligned (its status word is cleared first).  No synchronisation.
  */
 MAO_API mao_status mao_test_wait_timeout(void* workspace, size_t ws_bytes, mao_stream_t stream);
+
+/*
+ * How a launch of the linear layer's products (mao_linear, mao_linear_backward) is cut and dealt;
+ * host only, no GPU needed.  sizes: M, N, K of each of `products` products (one, or two with
+ * `backward`, the longer K first); workers: CTAs (pairs) of the grid.  plan receives the tile's
+ * edge, the plan's workers, and per product tiles_m, tiles_n, k-blocks of 64, whole tiles,
+ * slices of each other tile, k-blocks per slice.  dealt receives how often each work item comes
+ * up in the workers' lists: the first product's items, then the second's.  MAO_ERR_WORKSPACE:
+ * more items than dealt_bytes; MAO_ERR_UNSUPPORTED: a list names an item that is none.
+ */
+MAO_API mao_status mao_test_linear_deal(const int64_t* sizes, int32_t products, int32_t backward, int32_t workers,
+                                        int32_t* plan, uint8_t* dealt, size_t dealt_bytes);
+
+/* Writes what mao_layer_status reads on the current device, as a kernel's bounded wait would. */
+MAO_API mao_status mao_test_set_layer_status(int32_t code, int32_t where);
 
 MAO_API mao_status mao_test_gemm_workspace_size(int32_t kind, int32_t batch, int32_t M, int32_t N, int32_t K,
                                         size_t* bytes);

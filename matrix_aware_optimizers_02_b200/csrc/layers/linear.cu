@@ -2,6 +2,7 @@
 // the choice of tiles and K slices, and the launches.
 #include "act_bwd.h"
 #include "linear_gemm.cuh"
+#include "mao_testing.h"
 
 namespace mao {
 namespace {
@@ -438,4 +439,54 @@ extern "C" mao_status mao_layer_status(mao_stream_t stream, int32_t* where) {
     MAO_CUDA_TRY(cudaMemcpyToSymbol(g_layer_status, &clear, sizeof(clear)));
   }
   return static_cast<mao_status>(st.code);
+}
+
+// ------------------------------------------------------------------ verification
+namespace {
+template <int NP>
+void deal_out(const LinDeal& deal, int workers, uint8_t* dealt, const size_t (&from)[2], const size_t (&items)[2], size_t* stray) {
+  for (int w = 0; w < workers; ++w) {
+    LinWalk<NP> walk(w, workers);
+    for (int which = 0, item = 0; walk.next(deal, which, item);) {
+      if (item < 0 || (size_t)item >= items[which]) ++*stray;
+      else if (dealt[from[which] + item] < 255) ++dealt[from[which] + item];
+    }
+  }
+}
+}  // namespace
+
+extern "C" mao_status mao_test_linear_deal(const int64_t* sizes, int32_t products, int32_t backward, int32_t workers,
+                                           int32_t* plan, uint8_t* dealt, size_t dealt_bytes) {
+  if (sizes == nullptr || plan == nullptr || dealt == nullptr || workers < 1) return MAO_ERR_INVALID_ARG;
+  if (products < 1 || products > (backward ? 2 : 1)) return MAO_ERR_INVALID_ARG;
+  Shape q[2] = {};
+  for (int i = 0; i < products; ++i) {
+    q[i] = Shape{sizes[3 * i], sizes[3 * i + 1], sizes[3 * i + 2]};
+    if (q[i].M < 1 || q[i].N < 1 || q[i].K < 1 || std::max({q[i].M, q[i].N, q[i].K}) > (1ll << 30)) return MAO_ERR_SHAPE;
+  }
+  LinPlans plans;
+  if (!plan_of(q, products, &plans)) return MAO_ERR_SHAPE;
+  plan[0] = kTileEdge[plans.tile];
+  plan[1] = plans.deal.workers;
+  size_t from[2] = {0, 0}, items[2] = {0, 0}, total = 0, stray = 0;
+  for (int i = 0; i < products; ++i) {
+    const LinPlan& c = plans.p[i];
+    const int32_t put[6] = {c.tiles_m, c.tiles_n, c.nk, c.full, c.slices, c.slice_blocks};
+    std::memcpy(plan + 2 + 6 * i, put, sizeof(put));
+    const int slot = i + (backward ? 2 : 1) - products;  // as in products()
+    from[slot] = total;
+    items[slot] = (size_t)c.items();
+    total += items[slot];
+  }
+  if (total > dealt_bytes) return MAO_ERR_WORKSPACE;
+  std::memset(dealt, 0, total);
+  if (backward) deal_out<2>(plans.deal, workers, dealt, from, items, &stray);
+  else deal_out<1>(plans.deal, workers, dealt, from, items, &stray);
+  return stray == 0 ? MAO_OK : MAO_ERR_UNSUPPORTED;
+}
+
+extern "C" mao_status mao_test_set_layer_status(int32_t code, int32_t where) {
+  const DevStatus st = {code, where, 0, 0};
+  MAO_CUDA_TRY(cudaMemcpyToSymbol(g_layer_status, &st, sizeof(st)));
+  return MAO_OK;
 }

@@ -47,3 +47,12 @@ def test_checkpoints_of_another_type(api):
     zk = api.checkpoint8(dy.to(bf) * 1e5)
     dx, _, _ = api.linear_backward(dy.to(hf), x.to(hf).clamp(-1, 1), w.to(hf), z=zk, act="gelu")
     assert torch.isfinite(dx).all()
+
+
+def test_status_is_returned_once(api):
+    """What a bounded wait would record: the status and its site once, then nothing."""
+    from matrix_aware_optimizers_02_b200 import _lib as L
+    L.check(L.load().mao_test_set_layer_status(L.MAO_ERR_TIMEOUT, 53))
+    assert api.layer_status() == (L.MAO_ERR_TIMEOUT, 53)
+    assert api.layer_status() == (0, 0)
+    assert api.layer_status(torch.cuda.current_device()) == (0, 0)

@@ -155,3 +155,37 @@ def test_16_bit_results_of_long_one_signed_sums(api, dt):
     for r in range(0, rows, 16384):
         want += dy[r:r + 16384].double().t() @ x[r:r + 16384, :256].double()
     R.close(dw[:, :256], want, (1.01 * R.HALF_STEP[t] + 552 * R.TC) * want, "dw")
+
+
+def test_fp32_gradient_of_one_sign(api):
+    """A truncated add is off to one side, so a sum of one sign shows it in full.  16384 tokens:
+    parts of at most 12 k-blocks have 48 such adds of at most one step of what is summed so far
+    (half the part in the mean), and 16 products inside each; 22 parts are joined by rounded adds.
+    One sum of the whole K is off by 1.0e-4, sixteen times the bound."""
+    g = _gen(1)
+    t = torch.float16
+    rows, n, m = 16384, 2048, 4096
+    dy, x = _positive(g, rows, m, 0.5, 1.5, t), _positive(g, rows, n, 0.5, 1.5, t)
+    w = torch.zeros((m, n), dtype=t, device="cuda")
+    _, dw, _ = api.linear_backward(dy, x, w, need_dx=False, need_db=False)
+    want = dy.double().t() @ x.double()
+    R.close(dw, want, ((48 / 2 + 16) * R.TC + 23 * R.F32) * want, "dw")
+
+
+def test_kept_z_rounds_as_its_sums_do(api):
+    """Values of a kept z that round the other way than the exact z's: an error e of a sum does
+    that with probability |e| / step.  In the model of truncating adds the sums of parts of 11
+    k-blocks (K = 4096, unit results) are off by 5.9e-7 in the mean, one sum of the whole K by
+    4.0e-6 (553 such values, where the first expects 97); at most twice the first is allowed."""
+    g = _gen(2)
+    t = torch.bfloat16
+    rows, n, m = 2048, 4096, 2048
+    x = torch.randn((rows, n), generator=g, device="cuda").to(t)
+    w = (torch.randn((m, n), generator=g, device="cuda") * n ** -0.5).to(t)
+    _, kept = api.linear(x, w, checkpoint=True)
+    q, e = R.pack(x.double() @ w.double().t())
+    same = (kept.e == e).repeat_interleave(32, 1)
+    flips = int(((kept.q != q) & same).sum())
+    per = float((5.9e-7 / torch.exp2(e.double() - 127)).sum()) * 32
+    assert flips <= 2 * per + 5 * math.sqrt(2 * per), f"{flips} values round the other way, {per:.0f} expected"
+    assert int((~same).sum()) <= 32 * 32  # a block whose largest value lies that close to a power of two

@@ -1,15 +1,18 @@
 """Rules of the trained layers that a machine without a GPU can check: in the kernels' source,
 in the host's plans, and in the binding."""
 
+import ctypes
 import glob
 import os
 import re
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
+from matrix_aware_optimizers_02_b200 import _lib as L
 from matrix_aware_optimizers_02_b200 import layers
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -129,3 +132,52 @@ def test_binding_imports_without_cuda_in_torch():
     """The package's host side (layer sets, plans, refusals) works with a torch built for the CPU."""
     r = subprocess.run([sys.executable, "-c", _WITHOUT_CUDA], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "imported" in r.stdout, r.stdout + r.stderr
+
+
+def _deal(lib, sizes, backward, workers, room):
+    flat = (ctypes.c_int64 * 6)(*[v for s in sizes for v in s])
+    plan = (ctypes.c_int32 * 14)()
+    st = lib.mao_test_linear_deal(flat, len(sizes), int(backward), workers, plan, room.ctypes.data, room.nbytes)
+    return st, list(plan)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_every_work_item_is_dealt_once(seed):
+    """Random sizes of one product and of a gradient's two, on a B200's workers, on fewer, and on
+    an odd number: each tile, and each K slice of a sliced tile, is in exactly one list, and the
+    slices of a tile cover its K."""
+    lib = L.load()
+    rng = np.random.default_rng(seed)
+    room = np.zeros(1 << 22, dtype=np.uint8)
+
+    def size(low, high):
+        return int(round(np.exp(rng.uniform(np.log(low), np.log(high)))))
+
+    for _ in range(300):
+        rows, n, m = size(1, 70000), 8 * size(1, 2048), 8 * size(1, 2048)
+        dx, dw = (rows, n, m), (m, n, rows)
+        for sizes, backward in (([(rows, m, n)], 0), ([dx], 1), ([dw], 1), ([dx, dw] if m >= rows else [dw, dx], 1)):
+            for grid in (None, 1, 37):
+                st, plan = _deal(lib, sizes, backward, grid or 74, room)
+                if grid is None and plan[1] != 74:
+                    st, plan = _deal(lib, sizes, backward, plan[1], room)
+                assert st == L.MAO_OK, (sizes, backward, grid)
+                edge, items = plan[0], 0
+                for i, (M, N, K) in enumerate(sizes):
+                    tm, tn, nk, full, slices, blocks = plan[2 + 6 * i:8 + 6 * i]
+                    assert (tm, tn, nk) == (-(-M // edge), -(-N // edge), -(-K // 64))
+                    assert 0 <= full <= tm * tn and slices >= 1
+                    if slices > 1:  # the last slice is not empty
+                        assert (slices - 1) * blocks < nk <= slices * blocks
+                    items += full + (tm * tn - full) * slices
+                assert (room[:items] == 1).all(), (sizes, backward, grid, np.unique(room[:items], return_counts=True))
+
+
+def test_deal_refusals():
+    lib = L.load()
+    room = np.zeros(4, dtype=np.uint8)
+    assert _deal(lib, [(256, 256, 64)], 0, 74, room)[0] == L.MAO_OK
+    assert _deal(lib, [(4096, 4096, 64)], 0, 74, room)[0] == L.MAO_ERR_WORKSPACE
+    assert _deal(lib, [(0, 256, 64)], 0, 74, room)[0] == L.MAO_ERR_SHAPE
+    assert _deal(lib, [(256, 256, 64)], 0, 0, room)[0] == L.MAO_ERR_INVALID_ARG
+    assert _deal(lib, [(256, 256, 64)] * 2, 0, 74, room)[0] == L.MAO_ERR_INVALID_ARG
