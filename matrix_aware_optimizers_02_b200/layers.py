@@ -35,9 +35,7 @@ _NO_CKPT = L.Ckpt8(None, None, 0, 0)
 
 
 def _has_tangent(t: torch.Tensor) -> bool:
-    # outside a dual level, which is nearly always, one comparison; no_grad leaves forward mode on
-    return (getattr(forward_ad, "_current_level", 0) >= 0 and torch._C._is_fwd_grad_enabled() and
-            forward_ad.unpack_dual(t).tangent is not None)
+    return torch._C._is_fwd_grad_enabled() and forward_ad.unpack_dual(t).tangent is not None
 
 
 def _check(name: str, t: torch.Tensor, device=None, dtype=None) -> None:
@@ -51,7 +49,8 @@ def _check(name: str, t: torch.Tensor, device=None, dtype=None) -> None:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: these calls record no graph (use torch.no_grad() or detach())")
-    if _has_tangent(t):
+    # no_grad leaves forward mode on; outside a dual level, which is nearly always, one comparison
+    if getattr(forward_ad, "_current_level", 0) >= 0 and _has_tangent(t):
         raise ValueError(f"{name} carries a forward-mode tangent: these calls have none (use unpack_dual(...).primal)")
 
 
