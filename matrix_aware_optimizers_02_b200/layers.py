@@ -356,7 +356,7 @@ def linear_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8], W: to
     xp, ld_x, xc = _check_kept("x", x, (rows, n), dev, dt)
     if need_dw and dt == torch.float16 and isinstance(x, Checkpoint8) and x.dtype != dt:
         raise TypeError(f"x is a checkpoint of {x.dtype} values, which the product dz^T x would read as {dt}: above "
-                        f"65504 they would be infinite")
+                        f"65504 they would be infinite (Checkpoint8(x.q, x.e, x.cols, {dt}) says that they are not)")
     zp, ld_z, zc = None, 0, _NO_CKPT
     if a_id:
         if z is None:
